@@ -24,7 +24,10 @@ __all__ = ["NF4Weight", "QLORA_QT_NF4", "QLORA_QT_FP4", "QLORA_FMT_BLOCK128", "Q
            "qlora_lora_linear_bwd_dx", "qlora_lora_grad_AB",
            "qlora_sync_status", "qlora_set_wait_limit_ns", "qlora_probe_wait_timeout", "Q80Weight",
            "qlora_q8_0_packed_bytes", "qlora_quantize_q8_0", "qlora_dequant_q8_0", "qlora_q8_0_lora_linear_fwd",
-           "qlora_q8_0_lora_linear_bwd_dx", "QloraError"]
+           "qlora_q8_0_lora_linear_bwd_dx",
+           "qlora_embed_fwd", "qlora_embed_nf4_fwd", "qlora_embed_q8_0_fwd", "qlora_embed_grad_workspace_bytes",
+           "qlora_embed_grad", "AdamWTensor", "AdamWPlan", "qlora_adamw_plan_init", "qlora_adamw_step",
+           "qlora_grad_norm", "qlora_adam8_encode", "qlora_adam8_decode", "QloraError"]
 
 QloraError = _capi.QloraError
 
@@ -297,3 +300,222 @@ def qlora_q8_0_lora_linear_bwd_dx(weight: Q80Weight, dY, A, B, r: int, scaling: 
     _capi.check("qlora_q8_0_lora_linear_bwd_dx", _lib().qlora_q8_0_lora_linear_bwd_dx(
         ctypes.byref(s), _ptr(dY), M, _ptr(A), _ptr(B), int(r), float(scaling), _ptr(dX), _ptr(G_save), _ptr(ws),
         wsb, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- embedding
+
+def _here(*tensors) -> None:
+    """The calls launch on the current device: every tensor has to live there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _need_ids(ids) -> int:
+    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 1 or not ids.is_contiguous() or not ids.is_cuda:
+        raise ValueError(f"ids: expected contiguous cuda int32 or int64 [T], got {ids.dtype} {tuple(ids.shape)} on "
+                         f"{ids.device}")
+    return ids.element_size()
+
+
+def _need_float(t, shape, name) -> int:
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    _need(t, t.dtype, shape, name)
+    return int(t.dtype == torch.bfloat16)
+
+
+def qlora_embed_fwd(table: torch.Tensor, ids: torch.Tensor, scale: float, Y: torch.Tensor, stream=None) -> None:
+    """Y [T, H] = scale * table[ids] from a float32 or bfloat16 table [V, H]."""
+    if table.dim() != 2:
+        raise ValueError("table must be [V, H]")
+    V, H = table.shape
+    idb, tb = _need_ids(ids), _need_float(table, (V, H), "table")
+    yb = _need_float(Y, (ids.shape[0], H), "Y")
+    _here(table, ids, Y)
+    _capi.check("qlora_embed_fwd", _lib().qlora_embed_fwd(table.data_ptr(), tb, V, H, ids.data_ptr(), idb, ids.shape[0],
+                                                          scale, Y.data_ptr(), yb, _stream(stream)))
+
+
+def _embed_packed(name, weight, ids, scale, Y, stream):
+    idb = _need_ids(ids)
+    yb = _need_float(Y, (ids.shape[0], weight.n_in), "Y")
+    _here(ids, Y)
+    s = weight.c_struct()
+    _capi.check(name, getattr(_lib(), name)(ctypes.byref(s), ids.data_ptr(), idb, ids.shape[0], scale, Y.data_ptr(), yb,
+                                            _stream(stream)))
+
+
+def qlora_embed_nf4_fwd(weight: NF4Weight, ids: torch.Tensor, scale: float, Y: torch.Tensor, stream=None) -> None:
+    """Y [T, n_in] = scale * the dequantized rows `ids` of a packed 4-bit table, as float32 or bfloat16."""
+    _here(weight.codes, weight.scales)
+    _embed_packed("qlora_embed_nf4_fwd", weight, ids, scale, Y, stream)
+
+
+def qlora_embed_q8_0_fwd(weight: Q80Weight, ids: torch.Tensor, scale: float, Y: torch.Tensor, stream=None) -> None:
+    """Y [T, n_in] = scale * the dequantized rows `ids` of a Q8_0 table, as float32 or bfloat16."""
+    _here(weight.q, weight.d)
+    _embed_packed("qlora_embed_q8_0_fwd", weight, ids, scale, Y, stream)
+
+
+def qlora_embed_grad_workspace_bytes(T: int, V: int, H: int) -> int:
+    return int(_lib().qlora_embed_grad_workspace_bytes(int(T), int(V), int(H)))
+
+
+def qlora_embed_grad(ids: torch.Tensor, dY: torch.Tensor, scale: float, dE: torch.Tensor, padding_id: int = -1,
+                     accumulate: bool = False, ws=None, stream=None) -> None:
+    """dE [V, H] = scale * the sum of dY's rows by token id (added to dE with accumulate); dY and dE are
+    float32 or bfloat16, `ws` a scratch tensor of qlora_embed_grad_workspace_bytes(T, V, H)."""
+    if dE.dim() != 2:
+        raise ValueError("dE must be [V, H]")
+    V, H = dE.shape
+    T = ids.shape[0]
+    idb, yb, eb = _need_ids(ids), _need_float(dY, (T, H), "dY"), _need_float(dE, (V, H), "dE")
+    _here(ids, dY, dE, ws)
+    wsb = 0 if ws is None else ws.numel() * ws.element_size()
+    _capi.check("qlora_embed_grad", _lib().qlora_embed_grad(
+        ids.data_ptr(), idb, T, dY.data_ptr(), yb, V, H, scale, int(padding_id), dE.data_ptr(), eb,
+        int(bool(accumulate)), None if ws is None else ws.data_ptr(), wsb, _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- optimizer
+
+@dataclass
+class AdamWTensor:
+    """One trained tensor of an AdamW plan: contiguous device buffers owned by the caller.
+
+    param: float32 or bfloat16, updated in place; None with a grad alone makes a tensor that only counts in
+    qlora_grad_norm.  exp_avg / exp_avg_sq: float32 m and v, or int8 / uint8 codes with their float32 block
+    steps exp_avg_step / exp_avg_sq_step [ceil(numel / 256)] (8-bit states; all zeros is the start).
+    param_bf16: bfloat16 copy written beside a float32 param (the A or B that the layer reads).  lr_scale
+    multiplies the step's learning rate for this tensor."""
+    param: torch.Tensor | None
+    grad: torch.Tensor
+    exp_avg: torch.Tensor | None = None
+    exp_avg_sq: torch.Tensor | None = None
+    exp_avg_step: torch.Tensor | None = None
+    exp_avg_sq_step: torch.Tensor | None = None
+    param_bf16: torch.Tensor | None = None
+    lr_scale: float = 1.0
+    weight_decay: float = 0.0
+
+    @classmethod
+    def zeros(cls, param: torch.Tensor, grad: torch.Tensor, bits: int = 32, **kw) -> "AdamWTensor":
+        """The tensor with zero states of 32 or 8 bits."""
+        if bits not in (8, 32):
+            raise ValueError("bits must be 8 or 32")
+        n, dev = param.numel(), param.device
+        if bits == 32:
+            return cls(param, grad, *(torch.zeros(n, dtype=torch.float32, device=dev) for _ in range(2)), **kw)
+        return cls(param, grad, torch.zeros(n, dtype=torch.int8, device=dev),
+                   torch.zeros(n, dtype=torch.uint8, device=dev),
+                   *(torch.zeros((n + 255) // 256, dtype=torch.float32, device=dev) for _ in range(2)), **kw)
+
+    def c_struct(self) -> _capi.AdamWTensorC:
+        n = self.grad.numel()
+        flat = lambda t, dtypes, name, k=n: _need_flat(t, dtypes, k, name)  # noqa: E731
+        flags = _capi.OPT_GRAD_BF16 if flat(self.grad, (torch.float32, torch.bfloat16), "grad") == torch.bfloat16 else 0
+        if self.param is None:
+            if any(t is not None for t in (self.exp_avg, self.exp_avg_sq, self.param_bf16)):
+                raise ValueError("a tensor without param has a grad alone")
+            return _capi.AdamWTensorC(grad=self.grad.data_ptr(), numel=n, flags=flags | _capi.OPT_GRAD_ONLY)
+        if flat(self.param, (torch.float32, torch.bfloat16), "param") == torch.bfloat16:
+            flags |= _capi.OPT_PARAM_BF16
+        steps = [None, None]
+        if flat(self.exp_avg, (torch.float32, torch.int8), "exp_avg") == torch.int8:
+            flags |= _capi.OPT_STATE_8BIT
+            flat(self.exp_avg_sq, (torch.uint8,), "exp_avg_sq")
+            for name in ("exp_avg_step", "exp_avg_sq_step"):
+                flat(getattr(self, name), (torch.float32,), name, (n + 255) // 256)
+            steps = [self.exp_avg_step.data_ptr(), self.exp_avg_sq_step.data_ptr()]
+        else:
+            flat(self.exp_avg_sq, (torch.float32,), "exp_avg_sq")
+        if self.param_bf16 is not None:
+            flat(self.param_bf16, (torch.bfloat16,), "param_bf16")
+        return _capi.AdamWTensorC(self.param.data_ptr(), None if self.param_bf16 is None else self.param_bf16.data_ptr(),
+                                  self.grad.data_ptr(), self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), *steps, n,
+                                  float(self.lr_scale), float(self.weight_decay), flags, 0)
+
+
+def _need_flat(t, dtypes, n, name):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype not in dtypes or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected contiguous cuda {' or '.join(map(str, dtypes))} of {n} elements, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    _here(t)
+    return t.dtype
+
+
+@dataclass
+class AdamWPlan:
+    """A list of tensors prepared for qlora_adamw_step and qlora_grad_norm; keeps the tensors and the device
+    buffer alive.  Made by qlora_adamw_plan_init."""
+    tensors: list
+    buffer: torch.Tensor
+    c_plan: _capi.AdamWPlanC
+
+
+def qlora_adamw_plan_init(tensors, stream=None) -> AdamWPlan:
+    tensors = list(tensors)
+    if not tensors:
+        raise ValueError("a plan needs a tensor")
+    arr = (_capi.AdamWTensorC * len(tensors))(*(t.c_struct() for t in tensors))
+    nbytes = _lib().qlora_adamw_plan_bytes(arr, len(tensors))
+    buffer = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device="cuda")
+    plan = AdamWPlan(tensors, buffer, _capi.AdamWPlanC())
+    _capi.check("qlora_adamw_plan_init", _lib().qlora_adamw_plan_init(arr, len(tensors), buffer.data_ptr(), buffer.numel(),
+                                                                      ctypes.byref(plan.c_plan), _stream(stream)))
+    return plan
+
+
+def _scalar(t, dtype, name):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != 1 or not t.is_cuda:
+        raise ValueError(f"{name}: expected one cuda {dtype}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    _here(t)
+    return t.data_ptr()
+
+
+def qlora_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999,
+                     eps: float = 1e-8, grad_scale=None, lr_dev=None, step_dev=None, stream=None) -> None:
+    """Step number `step` (from 1; 0 with a device counter step_dev) over the plan's tensors."""
+    _here(plan.buffer)
+    _capi.check("qlora_adamw_step", _lib().qlora_adamw_step(
+        ctypes.byref(plan.c_plan), lr, beta1, beta2, eps, step, _scalar(grad_scale, torch.float32, "grad_scale"),
+        _scalar(lr_dev, torch.float32, "lr_dev"), _scalar(step_dev, torch.int64, "step_dev"), _stream(stream)))
+
+
+def qlora_grad_norm(plan: AdamWPlan, max_norm: float, out: torch.Tensor, stream=None) -> None:
+    """out [2] float32 = the norm of the plan's gradients and the clip coefficient (pass out[1:2] as grad_scale)."""
+    _need(out, torch.float32, (2,), "out")
+    _here(plan.buffer, out)
+    _capi.check("qlora_grad_norm", _lib().qlora_grad_norm(ctypes.byref(plan.c_plan), max_norm, out.data_ptr(),
+                                                          _stream(stream)))
+
+
+def _adam8(codes, steps, x):
+    kind = {torch.int8: _capi.ADAM8_FIRST, torch.uint8: _capi.ADAM8_SECOND}.get(codes.dtype)
+    if kind is None:
+        raise ValueError("codes must be int8 (first moment) or uint8 (second moment)")
+    n = codes.numel()
+    _need_flat(codes, (codes.dtype,), n, "codes")
+    _need_flat(steps, (torch.float32,), (n + 255) // 256, "steps")
+    _need_flat(x, (torch.float32,), n, "x")
+    return kind, n
+
+
+def qlora_adam8_encode(x: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, stream=None) -> None:
+    """8-bit state of float32 moments x: m into int8 codes, or v into uint8 codes (of its root), with block steps."""
+    kind, n = _adam8(codes, steps, x)
+    _capi.check("qlora_adam8_encode", _lib().qlora_adam8_encode(x.data_ptr(), kind, codes.data_ptr(), steps.data_ptr(), n,
+                                                                _stream(stream)))
+
+
+def qlora_adam8_decode(codes: torch.Tensor, steps: torch.Tensor, x: torch.Tensor, stream=None) -> None:
+    """The float32 moments that an 8-bit state stands for: m from int8 codes, v from uint8 codes."""
+    kind, n = _adam8(codes, steps, x)
+    _capi.check("qlora_adam8_decode", _lib().qlora_adam8_decode(codes.data_ptr(), kind, steps.data_ptr(), x.data_ptr(), n,
+                                                                _stream(stream)))

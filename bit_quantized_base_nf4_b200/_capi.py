@@ -36,6 +36,24 @@ class Q80WeightC(ctypes.Structure):
 
 _QP = ctypes.POINTER(Q80WeightC)
 
+
+class AdamWTensorC(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("param_bf16", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_step", ctypes.c_void_p),
+                ("exp_avg_sq_step", ctypes.c_void_p), ("numel", ctypes.c_int64), ("lr_scale", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("flags", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamWPlanC(ctypes.Structure):
+    _fields_ = [("buffer", ctypes.c_void_p), ("chunks", ctypes.c_int64), ("tensors", ctypes.c_int64),
+                ("numel", ctypes.c_int64), ("grad_only", ctypes.c_int32), ("magic", ctypes.c_int32),
+                ("reserved", ctypes.c_int64)]
+
+
+OPT_PARAM_BF16, OPT_GRAD_BF16, OPT_STATE_8BIT, OPT_GRAD_ONLY = 1, 2, 4, 8
+ADAM8_FIRST, ADAM8_SECOND = 0, 1
+_f64, _TP, _PP = ctypes.c_double, ctypes.POINTER(AdamWTensorC), ctypes.POINTER(AdamWPlanC)
+
 SIGNATURES = {
     "qlora_packed_bytes": (_sz, [_i64]),
     "qlora_packed_bytes_fmt": (_sz, [_i64, ctypes.c_int32]),
@@ -58,6 +76,17 @@ SIGNATURES = {
     "qlora_q8_0_lora_linear_fwd": (_int, [_QP, _vp, _i64, _vp, _vp, _int, _f32, _vp, _vp, _vp, _sz, _vp]),
     "qlora_q8_0_lora_linear_bwd_dx": (_int, [_QP, _vp, _i64, _vp, _vp, _int, _f32, _vp, _vp, _vp, _sz, _vp]),
     "qlora_probe_wait_timeout": (_int, [_vp]),
+    "qlora_embed_nf4_fwd": (_int, [_WP, _vp, _int, _i64, _f32, _vp, _int, _vp]),
+    "qlora_embed_q8_0_fwd": (_int, [_QP, _vp, _int, _i64, _f32, _vp, _int, _vp]),
+    "qlora_embed_fwd": (_int, [_vp, _int, _i64, _i64, _vp, _int, _i64, _f32, _vp, _int, _vp]),
+    "qlora_embed_grad_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "qlora_embed_grad": (_int, [_vp, _int, _i64, _vp, _int, _i64, _i64, _f32, _i64, _vp, _int, _int, _vp, _sz, _vp]),
+    "qlora_adamw_plan_bytes": (_sz, [_TP, _i64]),
+    "qlora_adamw_plan_init": (_int, [_TP, _i64, _vp, _sz, _PP, _vp]),
+    "qlora_adamw_step": (_int, [_PP, _f64, _f64, _f64, _f64, _i64, _vp, _vp, _vp, _vp]),
+    "qlora_grad_norm": (_int, [_PP, _f32, _vp, _vp]),
+    "qlora_adam8_encode": (_int, [_vp, _int, _vp, _vp, _i64, _vp]),
+    "qlora_adam8_decode": (_int, [_vp, _int, _vp, _vp, _i64, _vp]),
 }
 
 _lib = None

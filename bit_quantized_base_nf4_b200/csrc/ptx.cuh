@@ -13,6 +13,7 @@ namespace qlora {
 __device__ int g_device_error = 0;
 constexpr int kDeviceErrTimeout = 6;
 constexpr int kDeviceErrTmemStore = 7;   // a TMEM store did not read back as written
+constexpr int kDeviceErrIndex = 8;       // a token id outside its table
 // Time after which a single pipeline wait gives up (ns of %globaltimer); 2 s unless
 // changed by qlora_set_wait_limit_ns.
 constexpr unsigned long long kDefaultWaitLimitNs = 2000000000ull;

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cstddef>
 #include <cstdint>
+#include <cstdlib>
 #include <mutex>
 
 #include "host_common.cuh"
@@ -14,6 +15,8 @@
 #include "fused_fwd_pair.cuh"
 #include "fused_bwd_pair.cuh"
 #include "decode_mma.cuh"
+#include "optimizer.cuh"
+#include "embedding.cuh"
 
 using namespace qlora;
 
@@ -584,6 +587,8 @@ qlora_status qlora_sync_status(void *stream) {
         cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int));
         if (v == kDeviceErrTmemStore)
             return fail(QLORA_ERR_CUDA, "a tensor-memory store did not read back as written (device error %d)", v);
+        if (v == kDeviceErrIndex)
+            return fail(QLORA_ERR_ARG, "a token id lies outside its embedding table (device error %d)", v);
         return fail(QLORA_ERR_TIMEOUT, "a kernel pipeline wait timed out (device error %d)", v);
     }
     return QLORA_OK;
@@ -946,6 +951,359 @@ qlora_status qlora_lora_grad_AB(const qlora_bf16 *X, const qlora_bf16 *dY, const
     QL_TRY(launch_skinny(X, 1, G, 1, M, K, r, scaling, dA, 1, K, st));
     QL_TRY(launch_skinny(dY, 1, U, 1, M, N, r, scaling, dB, r, 1, st));
     return QLORA_OK;
+}
+
+// ------------------------------------------------------------------ embedding
+
+static qlora_status check_ids(const void *ids, int ids_bytes, int64_t T, int64_t V, int64_t H) {
+    if (V <= 0 || H <= 0 || V > INT32_MAX || H > INT32_MAX) return fail(QLORA_ERR_SHAPE, "V and H must be in [1, 2^31)");
+    if (H % 8) return fail(QLORA_ERR_SHAPE, "the row length (%lld) must be a multiple of 8", (long long)H);
+    if (T < 0 || T > INT32_MAX) return fail(QLORA_ERR_SHAPE, "T (%lld) must be in [0, 2^31)", (long long)T);
+    if (ids_bytes != 4 && ids_bytes != 8) return fail(QLORA_ERR_ARG, "ids_bytes must be 4 (int32) or 8 (int64)");
+    if (T > 0 && !ids) return fail(QLORA_ERR_ARG, "ids is NULL");
+    if (reinterpret_cast<uintptr_t>(ids) % ids_bytes)
+        return fail(QLORA_ERR_ALIGN, "ids must be aligned to its elements (%d bytes)", ids_bytes);
+    return QLORA_OK;
+}
+
+}  // extern "C" (a template has no C linkage)
+
+template <int kTable>
+static qlora_status launch_embed_fwd(emb::FwdArgs &a, const void *ids, int ids_bytes, int64_t T, int64_t V, int64_t H,
+                                     float scale, void *Y, int y_is_bf16, void *stream) {
+    QL_TRY(check_ids(ids, ids_bytes, T, V, H));
+    if (y_is_bf16 != 0 && y_is_bf16 != 1) return fail(QLORA_ERR_ARG, "y_is_bf16 must be 0 or 1");
+    if (!std::isfinite(scale)) return fail(QLORA_ERR_ARG, "scale must be finite");
+    if (T == 0) return QLORA_OK;
+    if (!Y) return fail(QLORA_ERR_ARG, "Y is NULL");
+    if (!aligned16(Y)) return fail(QLORA_ERR_ALIGN, "Y must be 16-byte aligned");
+    a.segs = static_cast<int>(ceil_div(H, emb::kRun));
+    const int64_t grid = ceil_div(T * a.segs, emb::kFwdThreads / 32);
+    if (grid > INT32_MAX) return fail(QLORA_ERR_SHAPE, "T x H is too large for one call");
+    QL_TRY(require_sm100());
+    a.ids = emb::Ids{ids, ids_bytes == 8};
+    a.out = Y;
+    a.T = T;
+    a.V = V;
+    a.H = H;
+    a.scale = scale;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (y_is_bf16) emb::embed_fwd_kernel<kTable, true><<<static_cast<unsigned>(grid), emb::kFwdThreads, 0, st>>>(a);
+    else emb::embed_fwd_kernel<kTable, false><<<static_cast<unsigned>(grid), emb::kFwdThreads, 0, st>>>(a);
+    return launch_check("embed_fwd_kernel launch");
+}
+
+extern "C" {
+
+qlora_status qlora_embed_nf4_fwd(const qlora_nf4_weight *w, const void *ids, int ids_bytes, int64_t T, float scale,
+                                 void *Y, int y_is_bf16, void *stream) {
+    QL_TRY(check_weight(w));
+    emb::FwdArgs a = {};
+    a.table = w->codes;
+    a.sc = scale_src(w);
+    const Codebook &cb = codebook_for(w->quant_type);
+    for (int i = 0; i < 16; ++i) a.level[i] = cb.level[i];
+    return launch_embed_fwd<emb::kTableNf4>(a, ids, ids_bytes, T, w->n_out, w->n_in, scale, Y, y_is_bf16, stream);
+}
+
+qlora_status qlora_embed_q8_0_fwd(const qlora_q8_0_weight *w, const void *ids, int ids_bytes, int64_t T, float scale,
+                                  void *Y, int y_is_bf16, void *stream) {
+    QL_TRY(check_q8(w));
+    emb::FwdArgs a = {};
+    a.table = w->q;
+    a.d8 = w->d;
+    return launch_embed_fwd<emb::kTableQ8>(a, ids, ids_bytes, T, w->n_out, w->n_in, scale, Y, y_is_bf16, stream);
+}
+
+qlora_status qlora_embed_fwd(const void *E, int e_is_bf16, int64_t V, int64_t H, const void *ids, int ids_bytes,
+                             int64_t T, float scale, void *Y, int y_is_bf16, void *stream) {
+    if (!E) return fail(QLORA_ERR_ARG, "E is NULL");
+    if (!aligned16(E)) return fail(QLORA_ERR_ALIGN, "E must be 16-byte aligned");
+    if (e_is_bf16 != 0 && e_is_bf16 != 1) return fail(QLORA_ERR_ARG, "e_is_bf16 must be 0 or 1");
+    emb::FwdArgs a = {};
+    a.table = E;
+    if (e_is_bf16) return launch_embed_fwd<emb::kTableBf16>(a, ids, ids_bytes, T, V, H, scale, Y, y_is_bf16, stream);
+    return launch_embed_fwd<emb::kTableF32>(a, ids, ids_bytes, T, V, H, scale, Y, y_is_bf16, stream);
+}
+
+// Sorted tokens per chunk of the gradient's reduction: a power of two in [8, 64], about eight blocks per
+// SM (148) where T allows it; longer chunks leave fewer partial sums, shorter ones more blocks.
+static int embed_chunk(int64_t T, int64_t H) {
+    const int64_t want = T * ceil_div(H, emb::kRedCols) / (8 * 148);
+    int c = 8;
+    while (c < emb::kMaxChunk && 2 * c <= want) c *= 2;
+    return c;
+}
+
+size_t qlora_embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t H) {
+    if (T < 0 || V <= 0 || H <= 0 || T > INT32_MAX || V > INT32_MAX || H > INT32_MAX || H % 8) return 0;
+    return std::max<size_t>(256, 4 * round256(size_t(T) * 4) + size_t(ceil_div(T, embed_chunk(T, H))) * 2 * size_t(H) * 4);
+}
+
+qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const void *dY, int dy_is_bf16, int64_t V,
+                              int64_t H, float scale, int64_t padding_id, void *dE, int de_is_bf16, int accumulate,
+                              void *ws, size_t ws_bytes, void *stream) {
+    QL_TRY(check_ids(ids, ids_bytes, T, V, H));
+    if (!dE || (T > 0 && !dY)) return fail(QLORA_ERR_ARG, "dY and dE must be non-NULL");
+    if (!aligned16(dY) || !aligned16(dE)) return fail(QLORA_ERR_ALIGN, "dY and dE must be 16-byte aligned");
+    if ((dy_is_bf16 | 1) != 1 || (de_is_bf16 | 1) != 1) return fail(QLORA_ERR_ARG, "dy_is_bf16 and de_is_bf16 must be 0 or 1");
+    if (accumulate != 0 && accumulate != 1) return fail(QLORA_ERR_ARG, "accumulate must be 0 or 1");
+    if (!std::isfinite(scale)) return fail(QLORA_ERR_ARG, "scale must be finite");
+    if (padding_id < -1 || padding_id >= V) return fail(QLORA_ERR_ARG, "padding_id (%lld) must be -1 or a row", (long long)padding_id);
+    QL_TRY(check_ws(ws, ws_bytes, T > 0 ? qlora_embed_grad_workspace_bytes(T, V, H) : 0));
+    if (T == 0 && accumulate) return QLORA_OK;
+    emb::GradArgs a = {};
+    a.ids = emb::Ids{ids, ids_bytes == 8};
+    a.T = T;
+    a.V = V;
+    a.H = H;
+    a.pad = padding_id;
+    uint8_t *wsb = static_cast<uint8_t *>(ws);
+    const size_t list = round256(size_t(T) * 4);
+    for (int i = 0; i < 2; ++i) {
+        a.key[i] = reinterpret_cast<uint32_t *>(wsb + list * i);
+        a.pos[i] = reinterpret_cast<uint32_t *>(wsb + list * (2 + i));
+    }
+    a.part = reinterpret_cast<float *>(wsb + 4 * list);
+    int nbits = 1;                                   // of the largest key, V
+    while ((V >> nbits) != 0) ++nbits;
+    a.passes = static_cast<int>(ceil_div(nbits, emb::kMaxBits));
+    a.bits = static_cast<int>(ceil_div(nbits, a.passes));
+    a.dY = dY;
+    a.dy_bf16 = dy_is_bf16;
+    a.dE = dE;
+    a.de_bf16 = de_is_bf16;
+    a.accumulate = accumulate;
+    a.scale = scale;
+    a.chunk = embed_chunk(T, H);
+    a.nchunks = ceil_div(T, a.chunk);
+    const int64_t tiles = ceil_div(H, emb::kRedCols), jtiles = ceil_div(H, emb::kJoinCols);
+    if (jtiles > 65535) return fail(QLORA_ERR_SHAPE, "H (%lld) must be at most %d", (long long)H, 65535 * emb::kJoinCols);
+    QL_TRY(require_sm100());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // one cluster sorts; when the whole table is written, a cluster per eight other SMs zeroes rows meanwhile
+    const int zero_clusters = accumulate ? 0 : std::max(1, sm_count() / emb::kSortCtas - 1);
+    QL_TRY(set_smem(emb::embed_sort_kernel, emb::kSortSmem));
+    emb::embed_sort_kernel<<<static_cast<unsigned>(emb::kSortCtas * (1 + zero_clusters)), emb::kSortThreads,
+                             emb::kSortSmem, st>>>(a);
+    QL_TRY(launch_check("embed_sort_kernel launch"));
+    if (T == 0) return QLORA_OK;
+    emb::embed_reduce_kernel<<<dim3(static_cast<unsigned>(a.nchunks), static_cast<unsigned>(tiles)), emb::kRedThreads, 0,
+                               st>>>(a);
+    QL_TRY(launch_check("embed_reduce_kernel launch"));
+    if (a.nchunks > 1) {
+        emb::embed_join_kernel<<<dim3(static_cast<unsigned>(ceil_div(a.nchunks - 1, emb::kJoinWarps)),
+                                      static_cast<unsigned>(jtiles)), emb::kJoinWarps * 32, 0, st>>>(a);
+        QL_TRY(launch_check("embed_join_kernel launch"));
+    }
+    return QLORA_OK;
+}
+
+// ------------------------------------------------------------------ optimizer
+
+static_assert(sizeof(qlora_adamw_tensor) == 80 && offsetof(qlora_adamw_tensor, flags) == 72, "ABI layout");
+static_assert(sizeof(qlora_adamw_plan) == 48, "ABI layout");
+constexpr int32_t kOptFlags = QLORA_OPT_PARAM_BF16 | QLORA_OPT_GRAD_BF16 | QLORA_OPT_STATE_8BIT | QLORA_OPT_GRAD_ONLY;
+constexpr int32_t kPlanMagic = 0x51504c4e;
+
+// Elements of a plan's chunk for `numel` in all: the largest multiple of 256 from 256 to 2048 that still
+// gives every warp of the device (64 per SM) a chunk.
+static int64_t plan_chunk(int64_t numel) {
+    int64_t c = 2048;
+    while (c > 256 && numel / c < 64 * 148) c /= 2;
+    return c;
+}
+
+static qlora_status check_opt_tensors(const qlora_adamw_tensor *ts, int64_t count, int64_t *numel) {
+    if (!ts) return fail(QLORA_ERR_ARG, "tensors is NULL");
+    if (count < 1 || count > INT32_MAX) return fail(QLORA_ERR_SHAPE, "count (%lld) must be in [1, 2^31)", (long long)count);
+    *numel = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const qlora_adamw_tensor &t = ts[i];
+        const long long k = (long long)i;
+        if (t.numel < 0 || t.numel > (int64_t(1) << 40)) return fail(QLORA_ERR_SHAPE, "tensor %lld: numel out of range", k);
+        if (t.flags & ~kOptFlags) return fail(QLORA_ERR_ARG, "tensor %lld: unknown flags (%d)", k, t.flags);
+        if (t.numel == 0) continue;
+        *numel += t.numel;
+        if (!t.grad) return fail(QLORA_ERR_ARG, "tensor %lld: grad is NULL", k);
+        if (!aligned16(t.grad)) return fail(QLORA_ERR_ALIGN, "tensor %lld: grad must be 16-byte aligned", k);
+        if (t.flags & QLORA_OPT_GRAD_ONLY) continue;
+        if (!t.param || !t.exp_avg || !t.exp_avg_sq) return fail(QLORA_ERR_ARG, "tensor %lld: param, exp_avg and exp_avg_sq must be non-NULL", k);
+        if (!aligned16(t.param) || !aligned16(t.exp_avg) || !aligned16(t.exp_avg_sq) || !aligned16(t.param_bf16))
+            return fail(QLORA_ERR_ALIGN, "tensor %lld: buffers must be 16-byte aligned", k);
+        if (t.param_bf16 && (t.flags & QLORA_OPT_PARAM_BF16))
+            return fail(QLORA_ERR_ARG, "tensor %lld: a bf16 copy goes with a float32 parameter only", k);
+        if (t.flags & QLORA_OPT_STATE_8BIT) {
+            if (!t.exp_avg_step || !t.exp_avg_sq_step) return fail(QLORA_ERR_ARG, "tensor %lld: 8-bit states need their block steps", k);
+            if (((reinterpret_cast<uintptr_t>(t.exp_avg_step) | reinterpret_cast<uintptr_t>(t.exp_avg_sq_step)) & 3) != 0)
+                return fail(QLORA_ERR_ALIGN, "tensor %lld: block steps must be 4-byte aligned", k);
+        }
+        if (!std::isfinite(t.lr_scale) || !std::isfinite(t.weight_decay) || t.lr_scale < 0 || t.weight_decay < 0)
+            return fail(QLORA_ERR_ARG, "tensor %lld: lr_scale and weight_decay must be finite and not negative", k);
+    }
+    return QLORA_OK;
+}
+
+static int64_t plan_chunks(const qlora_adamw_tensor *ts, int64_t count, int64_t chunk) {
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) n += ceil_div(ts[i].numel, chunk);
+    return n;
+}
+
+size_t qlora_adamw_plan_bytes(const qlora_adamw_tensor *tensors, int64_t count) {
+    int64_t numel = 0;
+    if (check_opt_tensors(tensors, count, &numel) != QLORA_OK) return 0;
+    return sizeof(optim::PlanHead) + size_t(plan_chunks(tensors, count, plan_chunk(numel))) * sizeof(optim::Chunk);
+}
+
+qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t count, void *buffer, size_t bytes,
+                                   qlora_adamw_plan *plan, void *stream) {
+    if (!plan) return fail(QLORA_ERR_ARG, "plan is NULL");
+    *plan = qlora_adamw_plan{};
+    int64_t numel = 0;
+    QL_TRY(check_opt_tensors(tensors, count, &numel));
+    const int64_t chunk = plan_chunk(numel), nchunks = plan_chunks(tensors, count, chunk);
+    const size_t need = sizeof(optim::PlanHead) + size_t(nchunks) * sizeof(optim::Chunk);
+    if (!buffer || bytes < need) return fail(QLORA_ERR_WORKSPACE, "the plan buffer holds %zu bytes, %zu needed", buffer ? bytes : size_t(0), need);
+    if (reinterpret_cast<uintptr_t>(buffer) % 256) return fail(QLORA_ERR_ALIGN, "the plan buffer must be 256-byte aligned");
+    QL_TRY(require_sm100());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    QL_TRY(cuda_check(cudaStreamIsCapturing(st, &cap), "cudaStreamIsCapturing"));
+    if (cap != cudaStreamCaptureStatusNone) return fail(QLORA_ERR_ARG, "a plan cannot be made during stream capture");
+    uint8_t *host = static_cast<uint8_t *>(std::calloc(1, need));
+    if (!host) return fail(QLORA_ERR_ARG, "no host memory for the plan (%zu bytes)", need);
+    optim::Chunk *c = reinterpret_cast<optim::Chunk *>(host + sizeof(optim::PlanHead));
+    int32_t grad_only = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const qlora_adamw_tensor &t = tensors[i];
+        const bool only = (t.flags & QLORA_OPT_GRAD_ONLY) != 0, eight = (t.flags & QLORA_OPT_STATE_8BIT) != 0;
+        if (only && t.numel) grad_only = 1;
+        const int64_t pb = (t.flags & QLORA_OPT_PARAM_BF16) ? 2 : 4, gb = (t.flags & QLORA_OPT_GRAD_BF16) ? 2 : 4, sb = eight ? 1 : 4;
+        auto at = [](const void *base, int64_t off) { return base ? uint64_t(reinterpret_cast<uintptr_t>(base)) + uint64_t(off) : 0; };
+        for (int64_t e = 0; e < t.numel; e += chunk, ++c) {
+            c->g = at(t.grad, e * gb);
+            c->n = static_cast<int32_t>(std::min(chunk, t.numel - e));
+            c->flags = uint32_t(t.flags) & (optim::kParamBf16 | optim::kGradBf16 | optim::kState8);
+            if (only) continue;
+            c->p = at(t.param, e * pb);
+            c->copy = at(t.param_bf16, e * 2);
+            c->m = at(t.exp_avg, e * sb);
+            c->v = at(t.exp_avg_sq, e * sb);
+            c->dm = eight ? at(t.exp_avg_step, e / optim::kBlock * 4) : 0;
+            c->dv = eight ? at(t.exp_avg_sq_step, e / optim::kBlock * 4) : 0;
+            c->lr_scale = t.lr_scale;
+            c->decay = t.weight_decay;
+        }
+    }
+    cudaError_t e = cudaMemcpyAsync(buffer, host, need, cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    std::free(host);
+    QL_TRY(cuda_check(e, "copy of the plan"));
+    plan->buffer = buffer;
+    plan->chunks = nchunks;
+    plan->tensors = count;
+    plan->numel = numel;
+    plan->grad_only = grad_only;
+    plan->magic = kPlanMagic;
+    return QLORA_OK;
+}
+
+static qlora_status check_plan(const qlora_adamw_plan *plan) {
+    if (!plan) return fail(QLORA_ERR_ARG, "plan is NULL");
+    if (plan->magic != kPlanMagic || !plan->buffer) return fail(QLORA_ERR_ARG, "plan was not made by qlora_adamw_plan_init");
+    return QLORA_OK;
+}
+static optim::PlanHead *plan_head(const qlora_adamw_plan *plan) { return static_cast<optim::PlanHead *>(plan->buffer); }
+static const optim::Chunk *plan_list(const qlora_adamw_plan *plan) {
+    return reinterpret_cast<const optim::Chunk *>(plan_head(plan) + 1);
+}
+// CTAs of a pass over the plan's chunks: enough warps for every chunk, at most `per_sm` CTAs per SM
+static unsigned plan_grid(const qlora_adamw_plan *plan, int per_sm) {
+    return static_cast<unsigned>(std::max<int64_t>(
+        1, std::min<int64_t>({ceil_div(plan->chunks, optim::kWarps), int64_t(per_sm) * sm_count(), optim::kPartials})));
+}
+
+qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double beta1, double beta2, double eps,
+                              int64_t step, const float *grad_scale, const float *lr_dev, int64_t *step_dev,
+                              void *stream) {
+    QL_TRY(check_plan(plan));
+    if (plan->grad_only) return fail(QLORA_ERR_ARG, "the plan holds QLORA_OPT_GRAD_ONLY tensors");
+    if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1)) return fail(QLORA_ERR_ARG, "betas must be in [0, 1)");
+    if (!(eps >= 0) || !std::isfinite(eps)) return fail(QLORA_ERR_ARG, "eps must be finite and not negative");
+    if (!lr_dev && !(lr >= 0 && std::isfinite(lr))) return fail(QLORA_ERR_ARG, "lr must be finite and not negative");
+    if (step_dev ? step != 0 : step < 1)
+        return fail(QLORA_ERR_ARG, "step (%lld) must be at least 1, or 0 with a step counter on the device", (long long)step);
+    if ((reinterpret_cast<uintptr_t>(grad_scale) | reinterpret_cast<uintptr_t>(lr_dev)) & 3 || reinterpret_cast<uintptr_t>(step_dev) & 7)
+        return fail(QLORA_ERR_ALIGN, "grad_scale, lr_dev and step_dev must be aligned to their types");
+    QL_TRY(require_sm100());
+    optim::StepArgs a = {};
+    a.chunks = plan_list(plan);
+    a.head = plan_head(plan);
+    a.coef = grad_scale;
+    a.lr_dev = lr_dev;
+    a.step_dev = step_dev;
+    a.beta1 = beta1;
+    a.beta2 = beta2;
+    a.nchunks = plan->chunks;
+    a.lr = lr_dev ? 0.f : static_cast<float>(lr);
+    a.b1 = static_cast<float>(beta1);
+    a.w1 = static_cast<float>(1.0 - beta1);
+    a.b2 = static_cast<float>(beta2);
+    a.w2 = static_cast<float>(1.0 - beta2);
+    a.eps = static_cast<float>(eps);
+    if (!step_dev) {
+        a.ibc1 = static_cast<float>(1.0 / (1.0 - std::pow(beta1, double(step))));
+        a.ibc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, double(step))));
+    }
+    optim::adamw_kernel<<<plan_grid(plan, 8), optim::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return launch_check("adamw_kernel launch");
+}
+
+qlora_status qlora_grad_norm(const qlora_adamw_plan *plan, float max_norm, float *out, void *stream) {
+    QL_TRY(check_plan(plan));
+    if (!(max_norm > 0)) return fail(QLORA_ERR_ARG, "max_norm must be positive (infinity for no limit)");
+    if (!out) return fail(QLORA_ERR_ARG, "out is NULL");
+    if (reinterpret_cast<uintptr_t>(out) & 3) return fail(QLORA_ERR_ALIGN, "out must be 4-byte aligned");
+    QL_TRY(require_sm100());
+    optim::grad_norm_kernel<<<plan_grid(plan, 8), optim::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        plan_list(plan), plan_head(plan), plan->chunks, max_norm, out);
+    return launch_check("grad_norm_kernel launch");
+}
+
+static qlora_status check_adam8(const void *codes, int kind, const float *steps, const float *x, int64_t numel) {
+    if (kind != QLORA_ADAM8_FIRST && kind != QLORA_ADAM8_SECOND) return fail(QLORA_ERR_ARG, "kind (%d) must be a QLORA_ADAM8_* value", kind);
+    if (numel < 0 || numel > (int64_t(1) << 40)) return fail(QLORA_ERR_SHAPE, "numel out of range");
+    if (numel == 0) return QLORA_OK;
+    if (!codes || !steps || !x) return fail(QLORA_ERR_ARG, "codes, steps and x must be non-NULL");
+    if (!aligned16(codes) || !aligned16(x)) return fail(QLORA_ERR_ALIGN, "codes and x must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(steps) & 3) return fail(QLORA_ERR_ALIGN, "steps must be 4-byte aligned");
+    return QLORA_OK;
+}
+static unsigned adam8_grid(int64_t numel) {
+    return static_cast<unsigned>(std::min<int64_t>(ceil_div(numel, optim::kBlock * optim::kWarps), int64_t(sm_count()) * 32));
+}
+
+qlora_status qlora_adam8_encode(const float *x, int kind, void *codes, float *steps, int64_t numel, void *stream) {
+    QL_TRY(check_adam8(codes, kind, steps, x, numel));
+    if (numel == 0) return QLORA_OK;
+    QL_TRY(require_sm100());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t *c = static_cast<uint8_t *>(codes);
+    if (kind == QLORA_ADAM8_SECOND) optim::adam8_encode_kernel<true><<<adam8_grid(numel), optim::kThreads, 0, st>>>(x, c, steps, numel);
+    else optim::adam8_encode_kernel<false><<<adam8_grid(numel), optim::kThreads, 0, st>>>(x, c, steps, numel);
+    return launch_check("adam8_encode_kernel launch");
+}
+
+qlora_status qlora_adam8_decode(const void *codes, int kind, const float *steps, float *x, int64_t numel, void *stream) {
+    QL_TRY(check_adam8(codes, kind, steps, x, numel));
+    if (numel == 0) return QLORA_OK;
+    QL_TRY(require_sm100());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const uint8_t *c = static_cast<const uint8_t *>(codes);
+    if (kind == QLORA_ADAM8_SECOND) optim::adam8_decode_kernel<true><<<adam8_grid(numel), optim::kThreads, 0, st>>>(c, steps, x, numel);
+    else optim::adam8_decode_kernel<false><<<adam8_grid(numel), optim::kThreads, 0, st>>>(c, steps, x, numel);
+    return launch_check("adam8_decode_kernel launch");
 }
 
 }  // extern "C"

@@ -280,10 +280,141 @@ qlora_status qlora_q8_0_lora_linear_bwd_dx(const qlora_q8_0_weight *w, const qlo
                                            qlora_bf16 *dX, qlora_bf16 *G_save, void *ws, size_t ws_bytes,
                                            void *stream);
 
+/* ------------------------------------------------------------------ embedding
+ * Rows of a table for a batch of token ids, and the gradient of a trained table.
+ * (The GGUF page, section 3.1, dequantizes the embedding on its own beside the
+ * layers; the pages give no kernel for it.)
+ *   ids : T token ids on the device, int32 (ids_bytes = 4) or int64 (8), aligned
+ *       to their size.  T = 0 is an empty batch.  An id outside [0, V) is never
+ *       followed: its output row is zero, it takes no part in the gradient, and
+ *       the next qlora_sync_status reports QLORA_ERR_ARG.
+ *   Rows have n_in (or H) elements, a multiple of 8.
+ * Y [T, n_in] receives scale * w' of row id_t, w' as qlora_dequant /
+ * qlora_dequant_q8_0 give it in float32: the product rounded to float32, and to
+ * bfloat16 ties-to-even when y_is_bf16 = 1.  Bit-exact.  Y must not overlap the
+ * table. */
+qlora_status qlora_embed_nf4_fwd(const qlora_nf4_weight *w, const void *ids, int ids_bytes, int64_t T, float scale,
+                                 void *Y, int y_is_bf16, void *stream);
+qlora_status qlora_embed_q8_0_fwd(const qlora_q8_0_weight *w, const void *ids, int ids_bytes, int64_t T, float scale,
+                                  void *Y, int y_is_bf16, void *stream);
+/* The same from a plain table E [V, H], float32 (e_is_bf16 = 0) or bfloat16 (1). */
+qlora_status qlora_embed_fwd(const void *E, int e_is_bf16, int64_t V, int64_t H, const void *ids, int ids_bytes,
+                             int64_t T, float scale, void *Y, int y_is_bf16, void *stream);
+
+/* Gradient of a plain table: dE[v, :] = scale * sum over the tokens t with
+ * id_t = v of dY[t, :], for every row of dE [V, H] (rows that no token names
+ * become zero), or added to the rows that tokens name when accumulate = 1 (the
+ * others are not touched).  dY [T, H] and dE are float32 or bfloat16
+ * (dy_is_bf16, de_is_bf16); sums are float32, rounded once to dE's type (with
+ * accumulate: the float32 sum of the old value and the scaled sum).  Tokens with
+ * id padding_id take no part (-1: none does).  The tokens are sorted by id, so
+ * equal ids add up in an order fixed by the ids: results repeat bit for bit.
+ * ws / ws_bytes: caller scratch of qlora_embed_grad_workspace_bytes(T, V, H); two
+ * calls whose work overlaps in time need a scratch each. */
+size_t qlora_embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t H);
+qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const void *dY, int dy_is_bf16, int64_t V,
+                              int64_t H, float scale, int64_t padding_id, void *dE, int de_is_bf16, int accumulate,
+                              void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ optimizer
+ * AdamW over many tensors in one launch: the update of A and B from the dA and
+ * dB of qlora_lora_grad_AB, and of any other trained tensor (the "5.8 QLoRA"
+ * page's optimizer paragraph and the "Quantized vs. non-quantized weights" page,
+ * section 4.3: AdamW with its states in 8 bits; the pages print no code table).
+ * Step t, per element, every operation rounded to float32:
+ *   g = grad * (*grad_scale)                     (grad alone without grad_scale)
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr lr_scale (weight_decay p + (m / (1 - beta1^t)) /
+ *                                         (sqrt(v) / sqrt(1 - beta2^t) + eps))
+ * 8-bit states hold blocks of 256 consecutive values (the last block of a tensor
+ * may be shorter) as k |k| d: one fp32 step d per block and an int8 k in
+ * -127..127 for m, a uint8 k in 0..255 for sqrt(v).  With K = 127 or 255 and
+ * RN = rounding to float32:
+ *   d = RN(max |x| / K^2),  y = RN(|x| RN(1 / d)),
+ *   |k| = the number of integers j >= 0 with y > j^2 + j + 1/2.
+ * d below 2^-126 is stored as 0 with k = 0; a block that holds an infinity or a
+ * NaN stores d = NaN and k = 0.  Reading back: m = RN(RN(k |k|) d),
+ * v = RN(w^2) with w = RN(k^2 d).  m, v and the codes are bit-exact (no fused
+ * multiply-add up to the code). */
+enum {
+    QLORA_OPT_PARAM_BF16 = 1, /* param is bfloat16, rounded to nearest once a step      */
+    QLORA_OPT_GRAD_BF16 = 2,  /* grad is bfloat16                                       */
+    QLORA_OPT_STATE_8BIT = 4, /* exp_avg and exp_avg_sq are codes with block steps      */
+    QLORA_OPT_GRAD_ONLY = 8   /* the tensor only counts in qlora_grad_norm              */
+};
+
+/* One tensor of a plan (80 bytes).  Buffers are contiguous device memory owned by
+ * the caller, 16-byte aligned (block steps: 4 bytes); tensors must not overlap.
+ * numel = 0 is an empty tensor, whose pointers are not looked at. */
+typedef struct {
+    void *param;            /* float32 or bfloat16 [numel], updated in place                  */
+    qlora_bf16 *param_bf16; /* bfloat16 copy written beside a float32 param (the A or B that
+                               the layer reads), or NULL                                      */
+    const void *grad;       /* float32 or bfloat16 [numel]                                    */
+    void *exp_avg;          /* m: float32 [numel], or int8 codes                              */
+    void *exp_avg_sq;       /* v: float32 [numel], or uint8 codes of sqrt(v)                  */
+    float *exp_avg_step;    /* 8-bit states: fp32 [ceil(numel / 256)]; else unused            */
+    float *exp_avg_sq_step;
+    int64_t numel;
+    float lr_scale;         /* factor on lr for this tensor                                   */
+    float weight_decay;
+    int32_t flags;          /* QLORA_OPT_*                                                    */
+    int32_t reserved;
+} qlora_adamw_tensor;
+
+/* A list of tensors prepared for the device; made by qlora_adamw_plan_init, read
+ * by the calls below, opaque to the caller. */
+typedef struct {
+    void *buffer;
+    int64_t chunks, tensors, numel;
+    int32_t grad_only, magic;
+    int64_t reserved;
+} qlora_adamw_plan;
+
+/* Bytes of the plan buffer for these tensors (host arithmetic only); 0 for a list
+ * that qlora_adamw_plan_init would refuse. */
+size_t qlora_adamw_plan_bytes(const qlora_adamw_tensor *tensors, int64_t count);
+
+/* Fills *plan (host) and `buffer` (device, 256-byte aligned, `bytes` of at least
+ * qlora_adamw_plan_bytes): the tensors' addresses cut into chunks.  `tensors` is
+ * a host array, free to go after the call.  Unlike the other calls it waits for
+ * `stream`, and it is refused during stream capture.  The plan stays good as long
+ * as the buffers it names stay where they are. */
+qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t count, void *buffer, size_t bytes,
+                                   qlora_adamw_plan *plan, void *stream);
+
+/* One AdamW step over the plan's tensors.
+ *   step: the number t >= 1 of this step; or 0 with step_dev, a device counter of
+ *     the steps taken so far: this call is step *step_dev + 1 and counts it.
+ *   lr_dev: device float32 that replaces lr, or NULL.  With step_dev and lr_dev a
+ *     captured call replays as the next step.
+ *   grad_scale: device float32, the clip coefficient (out + 1 of qlora_grad_norm),
+ *     or NULL.  A value that is not finite makes the step change nothing (the
+ *     counter included).
+ * 0 <= beta < 1, eps >= 0, lr >= 0.  The plan buffer holds scratch: two calls on
+ * one plan whose work overlaps in time race. */
+qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double beta1, double beta2, double eps,
+                              int64_t step, const float *grad_scale, const float *lr_dev, int64_t *step_dev,
+                              void *stream);
+
+/* out[0] = the 2-norm of all gradients of the plan together, out[1] = the clip
+ * coefficient min(1, max_norm / (norm + 1e-6)), NaN when the norm is not finite
+ * (device float32[2]).  Squares are summed in float64, in an order fixed by the
+ * plan.  max_norm > 0 (infinity: no limit).  Scratch as for qlora_adamw_step. */
+qlora_status qlora_grad_norm(const qlora_adamw_plan *plan, float max_norm, float *out, void *stream);
+
+/* The 8-bit state from and as float32 (loading and writing checkpoints): x [numel]
+ * float32 is m (QLORA_ADAM8_FIRST, int8 codes) or v (QLORA_ADAM8_SECOND, uint8
+ * codes of its root), steps fp32 [ceil(numel / 256)].  Bit-exact. */
+enum { QLORA_ADAM8_FIRST = 0, QLORA_ADAM8_SECOND = 1 };
+qlora_status qlora_adam8_encode(const float *x, int kind, void *codes, float *steps, int64_t numel, void *stream);
+qlora_status qlora_adam8_decode(const void *codes, int kind, const float *steps, float *x, int64_t numel, void *stream);
+
 /* Waits for `stream`, then reports and clears a device-side error recorded by
  * any earlier kernel of this library on the current device: a pipeline wait
- * that timed out (QLORA_ERR_TIMEOUT) or a tensor-memory store whose read-back
- * check failed (QLORA_ERR_CUDA). */
+ * that timed out (QLORA_ERR_TIMEOUT), a tensor-memory store whose read-back
+ * check failed (QLORA_ERR_CUDA) or a token id outside its table (QLORA_ERR_ARG). */
 qlora_status qlora_sync_status(void *stream);
 
 /* Message describing the last failure on the calling thread ("" if none). */
