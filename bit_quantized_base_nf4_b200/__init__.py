@@ -41,9 +41,9 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    # the raw handle of the current stream: building a torch.cuda.Stream object takes longer than a small kernel
+    raw = torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
+    return ctypes.c_void_p(raw)
 
 
 def _need(t, dtype, shape, name):
@@ -304,59 +304,69 @@ def qlora_q8_0_lora_linear_bwd_dx(weight: Q80Weight, dY, A, B, r: int, scaling: 
 
 # ----------------------------------------------------------------------------- embedding
 
-def _here(*tensors) -> None:
-    """The calls launch on the current device: every tensor has to live there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+def _on(t, dev: int, name: str) -> None:
+    """The calls launch on the current device: a tensor has to be contiguous and live there."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor on the current device cuda:{dev}, got strides {t.stride()} on "
+                         f"{t.device}")
 
 
-def _need_ids(ids) -> int:
-    if ids.dtype not in (torch.int32, torch.int64) or ids.dim() != 1 or not ids.is_contiguous() or not ids.is_cuda:
-        raise ValueError(f"ids: expected contiguous cuda int32 or int64 [T], got {ids.dtype} {tuple(ids.shape)} on "
-                         f"{ids.device}")
-    return ids.element_size()
+def _ids_bytes(ids, dev: int) -> int:
+    if ids.dtype is torch.int64:
+        size = 8
+    elif ids.dtype is torch.int32:
+        size = 4
+    else:
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    if ids.dim() != 1:
+        raise ValueError(f"ids must be [T], got {tuple(ids.shape)}")
+    _on(ids, dev, "ids")
+    return size
 
 
-def _need_float(t, shape, name) -> int:
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"{name} must be float32 or bfloat16")
-    _need(t, t.dtype, shape, name)
-    return int(t.dtype == torch.bfloat16)
+def _is_bf16(t, shape, dev: int, name: str) -> int:
+    """1 for a bfloat16 tensor of that shape on the device, 0 for a float32 one; else an error."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    _on(t, dev, name)
+    if t.dtype is torch.bfloat16:
+        return 1
+    if t.dtype is torch.float32:
+        return 0
+    raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
 def qlora_embed_fwd(table: torch.Tensor, ids: torch.Tensor, scale: float, Y: torch.Tensor, stream=None) -> None:
     """Y [T, H] = scale * table[ids] from a float32 or bfloat16 table [V, H]."""
+    dev = torch.cuda.current_device()
     if table.dim() != 2:
         raise ValueError("table must be [V, H]")
     V, H = table.shape
-    idb, tb = _need_ids(ids), _need_float(table, (V, H), "table")
-    yb = _need_float(Y, (ids.shape[0], H), "Y")
-    _here(table, ids, Y)
-    _capi.check("qlora_embed_fwd", _lib().qlora_embed_fwd(table.data_ptr(), tb, V, H, ids.data_ptr(), idb, ids.shape[0],
-                                                          scale, Y.data_ptr(), yb, _stream(stream)))
+    T = ids.numel()
+    idb, tb, yb = _ids_bytes(ids, dev), _is_bf16(table, (V, H), dev, "table"), _is_bf16(Y, (T, H), dev, "Y")
+    st = _lib().qlora_embed_fwd(table.data_ptr(), tb, V, H, ids.data_ptr(), idb, T, scale, Y.data_ptr(), yb, _stream(stream))
+    if st:
+        _capi.check("qlora_embed_fwd", st)
 
 
-def _embed_packed(name, weight, ids, scale, Y, stream):
-    idb = _need_ids(ids)
-    yb = _need_float(Y, (ids.shape[0], weight.n_in), "Y")
-    _here(ids, Y)
-    s = weight.c_struct()
-    _capi.check(name, getattr(_lib(), name)(ctypes.byref(s), ids.data_ptr(), idb, ids.shape[0], scale, Y.data_ptr(), yb,
-                                            _stream(stream)))
+def _embed_packed(name, f, weight, codes, ids, scale, Y, stream):
+    dev = torch.cuda.current_device()
+    T = ids.numel()
+    idb, yb = _ids_bytes(ids, dev), _is_bf16(Y, (T, weight.n_in), dev, "Y")
+    _on(codes, dev, "codes")
+    st = f(ctypes.byref(weight.c_struct()), ids.data_ptr(), idb, T, scale, Y.data_ptr(), yb, _stream(stream))
+    if st:
+        _capi.check(name, st)
 
 
 def qlora_embed_nf4_fwd(weight: NF4Weight, ids: torch.Tensor, scale: float, Y: torch.Tensor, stream=None) -> None:
     """Y [T, n_in] = scale * the dequantized rows `ids` of a packed 4-bit table, as float32 or bfloat16."""
-    _here(weight.codes, weight.scales)
-    _embed_packed("qlora_embed_nf4_fwd", weight, ids, scale, Y, stream)
+    _embed_packed("qlora_embed_nf4_fwd", _lib().qlora_embed_nf4_fwd, weight, weight.codes, ids, scale, Y, stream)
 
 
 def qlora_embed_q8_0_fwd(weight: Q80Weight, ids: torch.Tensor, scale: float, Y: torch.Tensor, stream=None) -> None:
     """Y [T, n_in] = scale * the dequantized rows `ids` of a Q8_0 table, as float32 or bfloat16."""
-    _here(weight.q, weight.d)
-    _embed_packed("qlora_embed_q8_0_fwd", weight, ids, scale, Y, stream)
+    _embed_packed("qlora_embed_q8_0_fwd", _lib().qlora_embed_q8_0_fwd, weight, weight.q, ids, scale, Y, stream)
 
 
 def qlora_embed_grad_workspace_bytes(T: int, V: int, H: int) -> int:
@@ -367,16 +377,19 @@ def qlora_embed_grad(ids: torch.Tensor, dY: torch.Tensor, scale: float, dE: torc
                      accumulate: bool = False, ws=None, stream=None) -> None:
     """dE [V, H] = scale * the sum of dY's rows by token id (added to dE with accumulate); dY and dE are
     float32 or bfloat16, `ws` a scratch tensor of qlora_embed_grad_workspace_bytes(T, V, H)."""
+    dev = torch.cuda.current_device()
     if dE.dim() != 2:
         raise ValueError("dE must be [V, H]")
     V, H = dE.shape
-    T = ids.shape[0]
-    idb, yb, eb = _need_ids(ids), _need_float(dY, (T, H), "dY"), _need_float(dE, (V, H), "dE")
-    _here(ids, dY, dE, ws)
-    wsb = 0 if ws is None else ws.numel() * ws.element_size()
-    _capi.check("qlora_embed_grad", _lib().qlora_embed_grad(
-        ids.data_ptr(), idb, T, dY.data_ptr(), yb, V, H, scale, int(padding_id), dE.data_ptr(), eb,
-        int(bool(accumulate)), None if ws is None else ws.data_ptr(), wsb, _stream(stream)))
+    T = ids.numel()
+    idb, yb, eb = _ids_bytes(ids, dev), _is_bf16(dY, (T, H), dev, "dY"), _is_bf16(dE, (V, H), dev, "dE")
+    if ws is not None:
+        _on(ws, dev, "ws")
+    st = _lib().qlora_embed_grad(
+        ids.data_ptr(), idb, T, dY.data_ptr(), yb, V, H, scale, padding_id, dE.data_ptr(), eb, 1 if accumulate else 0,
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    if st:
+        _capi.check("qlora_embed_grad", st)
 
 
 # ----------------------------------------------------------------------------- optimizer
@@ -413,38 +426,43 @@ class AdamWTensor:
                    *(torch.zeros((n + 255) // 256, dtype=torch.float32, device=dev) for _ in range(2)), **kw)
 
     def c_struct(self) -> _capi.AdamWTensorC:
-        n = self.grad.numel()
-        flat = lambda t, dtypes, name, k=n: _need_flat(t, dtypes, k, name)  # noqa: E731
-        flags = _capi.OPT_GRAD_BF16 if flat(self.grad, (torch.float32, torch.bfloat16), "grad") == torch.bfloat16 else 0
+        dev, n = torch.cuda.current_device(), self.grad.numel()
+        flags = _capi.OPT_GRAD_BF16 if _flat(self.grad, n, dev, _FLOATS, "grad") is torch.bfloat16 else 0
         if self.param is None:
-            if any(t is not None for t in (self.exp_avg, self.exp_avg_sq, self.param_bf16)):
+            if self.exp_avg is not None or self.exp_avg_sq is not None or self.param_bf16 is not None:
                 raise ValueError("a tensor without param has a grad alone")
-            return _capi.AdamWTensorC(grad=self.grad.data_ptr(), numel=n, flags=flags | _capi.OPT_GRAD_ONLY)
-        if flat(self.param, (torch.float32, torch.bfloat16), "param") == torch.bfloat16:
+            return _capi.AdamWTensorC(None, None, self.grad.data_ptr(), None, None, None, None, n, 0.0, 0.0,
+                                      flags | _capi.OPT_GRAD_ONLY, 0)
+        if _flat(self.param, n, dev, _FLOATS, "param") is torch.bfloat16:
             flags |= _capi.OPT_PARAM_BF16
-        steps = [None, None]
-        if flat(self.exp_avg, (torch.float32, torch.int8), "exp_avg") == torch.int8:
+        m_step = v_step = copy = None
+        if _flat(self.exp_avg, n, dev, _FIRST, "exp_avg") is torch.int8:
             flags |= _capi.OPT_STATE_8BIT
-            flat(self.exp_avg_sq, (torch.uint8,), "exp_avg_sq")
-            for name in ("exp_avg_step", "exp_avg_sq_step"):
-                flat(getattr(self, name), (torch.float32,), name, (n + 255) // 256)
-            steps = [self.exp_avg_step.data_ptr(), self.exp_avg_sq_step.data_ptr()]
+            _flat(self.exp_avg_sq, n, dev, _CODES, "exp_avg_sq")
+            nb = (n + 255) // 256
+            _flat(self.exp_avg_step, nb, dev, _F32, "exp_avg_step")
+            _flat(self.exp_avg_sq_step, nb, dev, _F32, "exp_avg_sq_step")
+            m_step, v_step = self.exp_avg_step.data_ptr(), self.exp_avg_sq_step.data_ptr()
         else:
-            flat(self.exp_avg_sq, (torch.float32,), "exp_avg_sq")
+            _flat(self.exp_avg_sq, n, dev, _F32, "exp_avg_sq")
         if self.param_bf16 is not None:
-            flat(self.param_bf16, (torch.bfloat16,), "param_bf16")
-        return _capi.AdamWTensorC(self.param.data_ptr(), None if self.param_bf16 is None else self.param_bf16.data_ptr(),
-                                  self.grad.data_ptr(), self.exp_avg.data_ptr(), self.exp_avg_sq.data_ptr(), *steps, n,
-                                  float(self.lr_scale), float(self.weight_decay), flags, 0)
+            _flat(self.param_bf16, n, dev, _BF16, "param_bf16")
+            copy = self.param_bf16.data_ptr()
+        return _capi.AdamWTensorC(self.param.data_ptr(), copy, self.grad.data_ptr(), self.exp_avg.data_ptr(),
+                                  self.exp_avg_sq.data_ptr(), m_step, v_step, n, self.lr_scale, self.weight_decay, flags, 0)
 
 
-def _need_flat(t, dtypes, n, name):
+_F32, _BF16, _FLOATS = (torch.float32,), (torch.bfloat16,), (torch.float32, torch.bfloat16)
+_FIRST, _CODES = (torch.float32, torch.int8), (torch.uint8,)
+
+
+def _flat(t, n: int, dev: int, dtypes, name: str):
+    """The type of a contiguous tensor of n elements on the device; an error for any other."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if t.dtype not in dtypes or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name}: expected contiguous cuda {' or '.join(map(str, dtypes))} of {n} elements, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    _here(t)
+    if t.dtype not in dtypes or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {' or '.join(map(str, dtypes))} of {n} elements on cuda:{dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.dtype
 
 
@@ -470,52 +488,55 @@ def qlora_adamw_plan_init(tensors, stream=None) -> AdamWPlan:
     return plan
 
 
-def _scalar(t, dtype, name):
+def _scalar(t, dtype, dev: int, name: str):
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != 1 or not t.is_cuda:
-        raise ValueError(f"{name}: expected one cuda {dtype}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    _here(t)
+    if t.dtype is not dtype or t.numel() != 1 or t.get_device() != dev:
+        raise ValueError(f"{name}: expected one {dtype} on cuda:{dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def qlora_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999,
                      eps: float = 1e-8, grad_scale=None, lr_dev=None, step_dev=None, stream=None) -> None:
     """Step number `step` (from 1; 0 with a device counter step_dev) over the plan's tensors."""
-    _here(plan.buffer)
-    _capi.check("qlora_adamw_step", _lib().qlora_adamw_step(
-        ctypes.byref(plan.c_plan), lr, beta1, beta2, eps, step, _scalar(grad_scale, torch.float32, "grad_scale"),
-        _scalar(lr_dev, torch.float32, "lr_dev"), _scalar(step_dev, torch.int64, "step_dev"), _stream(stream)))
+    dev = torch.cuda.current_device()
+    _on(plan.buffer, dev, "plan")
+    st = _lib().qlora_adamw_step(
+        ctypes.byref(plan.c_plan), lr, beta1, beta2, eps, step, _scalar(grad_scale, torch.float32, dev, "grad_scale"),
+        _scalar(lr_dev, torch.float32, dev, "lr_dev"), _scalar(step_dev, torch.int64, dev, "step_dev"), _stream(stream))
+    if st:
+        _capi.check("qlora_adamw_step", st)
 
 
 def qlora_grad_norm(plan: AdamWPlan, max_norm: float, out: torch.Tensor, stream=None) -> None:
     """out [2] float32 = the norm of the plan's gradients and the clip coefficient (pass out[1:2] as grad_scale)."""
-    _need(out, torch.float32, (2,), "out")
-    _here(plan.buffer, out)
-    _capi.check("qlora_grad_norm", _lib().qlora_grad_norm(ctypes.byref(plan.c_plan), max_norm, out.data_ptr(),
-                                                          _stream(stream)))
+    dev = torch.cuda.current_device()
+    _flat(out, 2, dev, _F32, "out")
+    _on(plan.buffer, dev, "plan")
+    st = _lib().qlora_grad_norm(ctypes.byref(plan.c_plan), max_norm, out.data_ptr(), _stream(stream))
+    if st:
+        _capi.check("qlora_grad_norm", st)
 
 
 def _adam8(codes, steps, x):
-    kind = {torch.int8: _capi.ADAM8_FIRST, torch.uint8: _capi.ADAM8_SECOND}.get(codes.dtype)
-    if kind is None:
-        raise ValueError("codes must be int8 (first moment) or uint8 (second moment)")
-    n = codes.numel()
-    _need_flat(codes, (codes.dtype,), n, "codes")
-    _need_flat(steps, (torch.float32,), (n + 255) // 256, "steps")
-    _need_flat(x, (torch.float32,), n, "x")
+    dev, n = torch.cuda.current_device(), codes.numel()
+    kind = _capi.ADAM8_SECOND if _flat(codes, n, dev, (torch.int8, torch.uint8), "codes") is torch.uint8 else _capi.ADAM8_FIRST
+    _flat(steps, (n + 255) // 256, dev, _F32, "steps")
+    _flat(x, n, dev, _F32, "x")
     return kind, n
 
 
 def qlora_adam8_encode(x: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, stream=None) -> None:
     """8-bit state of float32 moments x: m into int8 codes, or v into uint8 codes (of its root), with block steps."""
     kind, n = _adam8(codes, steps, x)
-    _capi.check("qlora_adam8_encode", _lib().qlora_adam8_encode(x.data_ptr(), kind, codes.data_ptr(), steps.data_ptr(), n,
-                                                                _stream(stream)))
+    st = _lib().qlora_adam8_encode(x.data_ptr(), kind, codes.data_ptr(), steps.data_ptr(), n, _stream(stream))
+    if st:
+        _capi.check("qlora_adam8_encode", st)
 
 
 def qlora_adam8_decode(codes: torch.Tensor, steps: torch.Tensor, x: torch.Tensor, stream=None) -> None:
     """The float32 moments that an 8-bit state stands for: m from int8 codes, v from uint8 codes."""
     kind, n = _adam8(codes, steps, x)
-    _capi.check("qlora_adam8_decode", _lib().qlora_adam8_decode(codes.data_ptr(), kind, steps.data_ptr(), x.data_ptr(), n,
-                                                                _stream(stream)))
+    st = _lib().qlora_adam8_decode(codes.data_ptr(), kind, steps.data_ptr(), x.data_ptr(), n, _stream(stream))
+    if st:
+        _capi.check("qlora_adam8_decode", st)

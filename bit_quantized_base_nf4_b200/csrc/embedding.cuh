@@ -18,9 +18,11 @@ struct Ids {
     const void *ptr;
     int is64;
 };
+// (Kernels here start before the preceding one has ended, so what that one may have written is read
+// through L2, not through the read-only path.)
 __device__ __forceinline__ int64_t id_at(const Ids &ids, int64_t t) {
-    return ids.is64 ? __ldg(reinterpret_cast<const long long *>(ids.ptr) + t)
-                    : int64_t(__ldg(reinterpret_cast<const int *>(ids.ptr) + t));
+    return ids.is64 ? __ldcg(reinterpret_cast<const long long *>(ids.ptr) + t)
+                    : int64_t(__ldcg(reinterpret_cast<const int *>(ids.ptr) + t));
 }
 __device__ __forceinline__ void report_bad_id() { atomicExch(&g_device_error, kDeviceErrIndex); }
 
@@ -37,15 +39,29 @@ struct FwdArgs {
     void *out;
     int64_t T, V, H;
     float scale;
-    int segs;              // row segments of kRun elements
+    int seg_shift;         // log2 of the row segments of kRun elements that a CTA takes (at most its warps)
     float level[16];
 };
 constexpr int kFwdThreads = 256;
+constexpr int kFwdWarps = kFwdThreads / 32;
 constexpr int kUnroll = 4;
 constexpr int kRun = 256 * kUnroll;   // elements of a row a warp takes: 8 per lane and step
 
+// scale words of the 64-weight run b64, as scale_load reads them
+__device__ __forceinline__ void scale_words(const ScaleSrc &s, int64_t b64, uint32_t &a, float &d) {
+    const int64_t b = b64 >> s.blk_shift;
+    if (s.dq) {
+        a = __ldcg(s.scales + b);
+        d = __ldcg(s.scales2 + (b >> 8));
+    } else {
+        a = __ldcg(reinterpret_cast<const uint32_t *>(s.scales) + b);
+        d = 1.f;
+    }
+}
+
 // A warp takes one segment of one token's row: its id, then every code and scale load of the
 // segment at once, 8 elements per lane and step, so that a bf16 output is one 16-byte store.
+// CTAs: x over tokens, y over groups of 2^seg_shift segments.
 template <int kTable, bool kOutBf16>
 __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const FwdArgs a) {
     __shared__ float s_lv[16];
@@ -57,11 +73,12 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const FwdArgs a)
         if (threadIdx.x < 16) s_lv[threadIdx.x] = lv;
         __syncthreads();
     }
-    const int lane = threadIdx.x & 31;
-    const int64_t task = int64_t(blockIdx.x) * (kFwdThreads / 32) + (threadIdx.x >> 5);
-    if (task >= a.T * a.segs) return;
-    const int64_t t = task / a.segs;
-    const int64_t e0 = (task - t * a.segs) * kRun + lane * 8;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = int64_t(blockIdx.x) * (kFwdWarps >> a.seg_shift) + (warp >> a.seg_shift);
+    const int64_t e0 = ((int64_t(blockIdx.y) << a.seg_shift) + (warp & ((1 << a.seg_shift) - 1))) * kRun + lane * 8;
+    if (t >= a.T) return;
     const int64_t id = id_at(a.ids, t);
     const bool ok = id >= 0 && id < a.V;
     if (!ok && lane == 0) report_bad_id();
@@ -79,18 +96,18 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const FwdArgs a)
         if (kTable == kTableF32) raw2[u] = make_uint4(0, 0, 0, 0);
         if (e < a.H && ok) {
             if (kTable == kTableNf4) {
-                raw[u].x = __ldg(reinterpret_cast<const uint32_t *>(a.table) + ((row + e) >> 3));
-                scale_load(a.sc, (row + e) >> 6, sa[u], sd[u]);
+                raw[u].x = __ldcg(reinterpret_cast<const uint32_t *>(a.table) + ((row + e) >> 3));
+                scale_words(a.sc, (row + e) >> 6, sa[u], sd[u]);
             } else if (kTable == kTableQ8) {
-                const uint2 q = __ldg(reinterpret_cast<const uint2 *>(a.table) + ((row + e) >> 3));
+                const uint2 q = __ldcg(reinterpret_cast<const uint2 *>(a.table) + ((row + e) >> 3));
                 raw[u].x = q.x;
                 raw[u].y = q.y;
-                sa[u] = __ldg(a.d8 + ((row + e) >> 5));
+                sa[u] = __ldcg(a.d8 + ((row + e) >> 5));
             } else if (kTable == kTableBf16) {
-                raw[u] = __ldg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 3));
+                raw[u] = __ldcg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 3));
             } else {
-                raw[u] = __ldg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 2));
-                raw2[u] = __ldg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 2) + 1);
+                raw[u] = __ldcg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 2));
+                raw2[u] = __ldcg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 2) + 1);
             }
         }
     }
@@ -148,17 +165,23 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const FwdArgs a)
 }
 
 // ------------------------------------------------------------------ gradient
-// dE[v, :] (+)= scale * sum over the tokens t with id_t = v of dY[t, :], in three launches:
-//   sort    the tokens by id (stable), and zero the rows that no token names;
+// dE[v, :] (+)= scale * sum over the tokens t with id_t = v of dY[t, :], in up to four launches:
+//   sort    the tokens by id (stable);
 //   reduce  equal runs of `chunk` sorted tokens each: an id that lies wholly in a chunk is summed
 //           and written, one that crosses a border leaves a partial sum per chunk;
-//   join    adds the partial sums of each such id in order and writes its row.
+//   join    adds the partial sums of each such id in order and writes its row;
+//   zero    (unless the gradient is added) zeroes the rows that no token names.
 // Every sum is float32, in an order fixed by the ids alone: results repeat bit for bit.
+// All four overlap: each starts once the one before it has (programmatic dependent launch).  `zero`
+// needs the ids only, not the sort, so the table's writes, nearly all of the time when the table is
+// large, run beside the sort and the reduction; it waits for the others at its end instead, so that
+// its completion means the whole call's.
 constexpr int kSortCtas = 8;            // one cluster sorts: bins and counts meet in shared memory
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBits = 9;             // bits of a digit: 512 bins
 constexpr int kMaxBins = 1 << kMaxBits;
+constexpr int kSortBatch = 4;           // rounds of 32 tokens whose loads a warp has in flight
 constexpr int kSortSmem = (kSortWarps * kMaxBins + 2 * kMaxBins + 64) * 4;
 
 struct GradArgs {
@@ -224,13 +247,22 @@ __device__ void sort_tokens(const GradArgs &a, uint32_t *smem) {
         const int shift = pass * a.bits;
         for (int b = lane; b < bins; b += 32) my[b] = 0;
         __syncwarp();
-        for (int64_t i = i_lo; i < i_hi; i += 32) {
-            const bool in = i + lane < i_hi;
-            const uint32_t k = in ? (pass ? __ldcg(src_k + i + lane) : key_of(a, i + lane)) : 0u;
-            const uint32_t d = in ? (k >> shift) & (bins - 1) : uint32_t(kMaxBins);   // idle lanes match none
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            if (in && (same & ((1u << lane) - 1u)) == 0) my[d] += __popc(same);
-            __syncwarp();
+        for (int64_t i = i_lo; i < i_hi; i += 32 * kSortBatch) {
+            uint32_t k[kSortBatch];
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u) {
+                const int64_t t = i + 32 * u + lane;
+                k[u] = t < i_hi ? (pass ? __ldcg(src_k + t) : key_of(a, t)) : 0u;
+            }
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u) {
+                if (i + 32 * u >= i_hi) break;
+                const bool in = i + 32 * u + lane < i_hi;
+                const uint32_t d = in ? (k[u] >> shift) & (bins - 1) : uint32_t(kMaxBins);   // idle lanes match none
+                const uint32_t same = __match_any_sync(0xffffffffu, d);
+                if (in && (same & ((1u << lane) - 1u)) == 0) my[d] += __popc(same);
+                __syncwarp();
+            }
         }
         __syncthreads();
         // per bin: counts of lower warps, and this CTA's total
@@ -269,108 +301,114 @@ __device__ void sort_tokens(const GradArgs &a, uint32_t *smem) {
             first[tid] = base;
         }
         __syncthreads();
-        for (int64_t i = i_lo; i < i_hi; i += 32) {
-            const bool in = i + lane < i_hi;
-            uint32_t k = 0, p = 0;
-            if (in) {
-                k = pass ? __ldcg(src_k + i + lane) : key_of(a, i + lane);
-                p = pass ? __ldcg(src_p + i + lane) : static_cast<uint32_t>(i + lane);
+        for (int64_t i = i_lo; i < i_hi; i += 32 * kSortBatch) {
+            uint32_t k[kSortBatch], p[kSortBatch];
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u) {
+                const int64_t t = i + 32 * u + lane;
+                k[u] = t < i_hi ? (pass ? __ldcg(src_k + t) : key_of(a, t)) : 0u;
+                p[u] = t < i_hi && pass ? __ldcg(src_p + t) : static_cast<uint32_t>(t);
             }
-            const uint32_t d = in ? (k >> shift) & (bins - 1) : uint32_t(kMaxBins);
-            const uint32_t same = __match_any_sync(0xffffffffu, d);
-            const uint32_t lower = same & ((1u << lane) - 1u);
-            uint32_t at = 0;
-            if (in) at = first[d] + my[d] + __popc(lower);
-            __syncwarp();
-            if (in && lower == 0) my[d] += __popc(same);
-            __syncwarp();
-            if (in) {
-                __stcg(dst_k + at, k);
-                __stcg(dst_p + at, p);
+#pragma unroll
+            for (int u = 0; u < kSortBatch; ++u) {
+                if (i + 32 * u >= i_hi) break;
+                const bool in = i + 32 * u + lane < i_hi;
+                const uint32_t d = in ? (k[u] >> shift) & (bins - 1) : uint32_t(kMaxBins);
+                const uint32_t same = __match_any_sync(0xffffffffu, d);
+                const uint32_t lower = same & ((1u << lane) - 1u);
+                uint32_t at = 0;
+                if (in) at = first[d] + my[d] + __popc(lower);
+                __syncwarp();
+                if (in && lower == 0) my[d] += __popc(same);
+                __syncwarp();
+                if (in) {
+                    __stcg(dst_k + at, k[u]);
+                    __stcg(dst_p + at, p[u]);
+                }
             }
         }
         cluster_barrier();   // the next pass reads what every CTA wrote; total is free again
     }
 }
 
-// Zeroes the rows of [lo, hi) that no token names: the CTA marks the named ones in a bitmap of at
-// most kMaskRows rows at a time, reading every id (from L2) for itself, so that it need not wait for the sort.
-constexpr int kMaskRows = kSortWarps * kMaxBins * 32;
-__device__ void zero_rows(const GradArgs &a, uint32_t *mask, int64_t lo, int64_t hi) {
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) embed_sort_kernel(const GradArgs a) {
+    extern __shared__ uint32_t sort_smem[];
+    pdl_wait();                 // before the release: what starts after this kernel may rely on the inputs
+    pdl_launch_dependents();
+    sort_tokens(a, sort_smem);
+}
+
+// Zero: a CTA owns an equal run of rows, marks the named ones in a bitmap (kMaskRows rows at a time,
+// reading every id from L2 for itself, so that it need not wait for the sort) and zeroes the others.
+constexpr int kZeroThreads = 512;
+constexpr int kMaskRows = 32768;
+__global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(const GradArgs a, int first) {
+    __shared__ uint32_t mask[kMaskRows / 32];
+    pdl_launch_dependents();
+    if (first) pdl_wait();      // no sort before this kernel: the inputs may still be on their way
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t row_bytes = a.H * (a.de_bf16 ? 2 : 4);
+    const int64_t row_words = a.H * (a.de_bf16 ? 2 : 4) / 16;
+    int64_t lo = a.V * blockIdx.x / gridDim.x;
+    const int64_t hi = a.V * (blockIdx.x + 1) / gridDim.x;
     for (; lo < hi; lo += kMaskRows) {
         const int64_t end = min(lo + int64_t(kMaskRows), hi);
-        const int words = static_cast<int>((end - lo + 31) / 32);
         __syncthreads();
-        for (int i = tid; i < words; i += kSortThreads) mask[i] = 0;
+        for (int i = tid; i < (end - lo + 31) / 32; i += kZeroThreads) mask[i] = 0;
         __syncthreads();
-        for (int64_t t = tid; t < a.T; t += kSortThreads) {
+#pragma unroll 8
+        for (int64_t t = tid; t < a.T; t += kZeroThreads) {
             const int64_t id = id_at(a.ids, t);
             if (id >= lo && id < end && id != a.pad) atomicOr(mask + ((id - lo) >> 5), 1u << ((id - lo) & 31));
         }
         __syncthreads();
-        for (int64_t r = lo + warp; r < end; r += kSortWarps) {
+        for (int64_t r = lo + warp; r < end; r += kZeroThreads / 32) {
             if ((mask[(r - lo) >> 5] >> ((r - lo) & 31)) & 1u) continue;
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(a.dE) + r * row_bytes);
-            for (int64_t i = lane; i < row_bytes / 16; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+            uint4 *dst = static_cast<uint4 *>(a.dE) + r * row_words;
+#pragma unroll 4
+            for (int64_t i = lane; i < row_words; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
+    if (!first) pdl_wait();
 }
 
-// Block roles: the first cluster sorts, the others zero.
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) embed_sort_kernel(const GradArgs a) {
-    extern __shared__ uint32_t sort_smem[];
-    if (blockIdx.x < kSortCtas) {
-        if (a.T > 0) sort_tokens(a, sort_smem);
-    } else {
-        const int64_t n = gridDim.x - kSortCtas, i = blockIdx.x - kSortCtas;
-        zero_rows(a, sort_smem, a.V * i / n, a.V * (i + 1) / n);
-    }
-}
-
-// 8 columns of dY row p from column c on, added to acc
-__device__ __forceinline__ void load_dy(const GradArgs &a, uint32_t p, int64_t c, uint4 *r) {
-    const int64_t o = int64_t(p) * a.H + c;
-    if (a.dy_bf16) {
-        r[0] = __ldg(reinterpret_cast<const uint4 *>(a.dY) + (o >> 3));
-    } else {
-        r[0] = __ldg(reinterpret_cast<const uint4 *>(a.dY) + (o >> 2));
-        r[1] = __ldg(reinterpret_cast<const uint4 *>(a.dY) + (o >> 2) + 1);
-    }
-}
-__device__ __forceinline__ void add_dy(const GradArgs &a, const uint4 *r, float *acc) {
-    const uint32_t x[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
-    if (a.dy_bf16) {
+// kN (4 or 8) elements of a row of dY or dE as loaded, and as floats
+template <bool kBf16, int kN>
+struct Raw {
+    static constexpr int kWords = kN / (kBf16 ? 2 : 1);
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const void *base, int64_t o) {
+        const char *p = static_cast<const char *>(base) + o * (kBf16 ? 2 : 4);
+        if (kWords == 2) {
+            const uint2 x = __ldcg(reinterpret_cast<const uint2 *>(p));
+            w[0] = x.x, w[1] = x.y;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            acc[2 * j] += __uint_as_float(x[j] << 16);
-            acc[2 * j + 1] += __uint_as_float(x[j] & 0xFFFF0000u);
-        }
-    } else {
-        const uint32_t y[4] = {r[1].x, r[1].y, r[1].z, r[1].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            acc[j] += __uint_as_float(x[j]);
-            acc[4 + j] += __uint_as_float(y[j]);
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            }
         }
     }
-}
-// dE[row, c .. c + kN) = (the old values +) scale * s, one rounding; kN = 4 or 8
-template <int kN>
-__device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64_t c, const float *s) {
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if (!kBf16) return __uint_as_float(w[i % kWords]);
+        return __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    }
+};
+// dE[row, c .. c + kN) = old + scale * s, one rounding (old: zeros when the gradient is written)
+template <bool kDeBf16, int kN>
+__device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64_t c, const float *s, const Raw<kDeBf16, kN> &old) {
     const int64_t o = int64_t(row) * a.H + c;
     float v[kN];
-    if (a.de_bf16) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = fmaf(a.scale, s[j], old.at(j));
+    if (kDeBf16) {
         uint2 *dst = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.dE) + o);
 #pragma unroll
         for (int h = 0; h < kN / 4; ++h) {
-            uint2 old = make_uint2(0, 0);
-            if (a.accumulate) old = dst[h];
-            v[4 * h] = fmaf(a.scale, s[4 * h], __uint_as_float(old.x << 16));
-            v[4 * h + 1] = fmaf(a.scale, s[4 * h + 1], __uint_as_float(old.x & 0xFFFF0000u));
-            v[4 * h + 2] = fmaf(a.scale, s[4 * h + 2], __uint_as_float(old.y << 16));
-            v[4 * h + 3] = fmaf(a.scale, s[4 * h + 3], __uint_as_float(old.y & 0xFFFF0000u));
             const __nv_bfloat162 lo = __floats2bfloat162_rn(v[4 * h], v[4 * h + 1]);
             const __nv_bfloat162 hi = __floats2bfloat162_rn(v[4 * h + 2], v[4 * h + 3]);
             dst[h] = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
@@ -378,22 +416,21 @@ __device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64
     } else {
         float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.dE) + o);
 #pragma unroll
-        for (int h = 0; h < kN / 4; ++h) {
-            float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (a.accumulate) old = dst[h];
-            dst[h] = make_float4(fmaf(a.scale, s[4 * h], old.x), fmaf(a.scale, s[4 * h + 1], old.y),
-                                 fmaf(a.scale, s[4 * h + 2], old.z), fmaf(a.scale, s[4 * h + 3], old.w));
-        }
+        for (int h = 0; h < kN / 4; ++h) dst[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
     }
 }
 
 // Reduce: block (chunk, column tile); a thread owns 8 columns and walks the chunk's tokens in order,
-// eight rows in flight.
+// kBatch rows of dY in flight, with the old rows of dE that they will be added to.
 constexpr int kRedThreads = 128;
 constexpr int kRedCols = kRedThreads * 8;
 constexpr int kMaxChunk = 64;
+constexpr int kBatch = 4;
+template <bool kDyBf16, bool kDeBf16, bool kAdd>
 __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArgs a) {
     __shared__ uint32_t s_id[kMaxChunk + 2], s_pos[kMaxChunk];   // s_id[0]: the token before the chunk; last + 1: after it
+    pdl_launch_dependents();
+    pdl_wait();
     const uint32_t *ids = a.key[a.passes & 1], *pos = a.pos[a.passes & 1];
     const int64_t ch = blockIdx.x;
     const int64_t i0 = ch * a.chunk;
@@ -401,36 +438,44 @@ __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArg
     constexpr uint32_t kNone = 0xFFFFFFFFu;
     for (int i = threadIdx.x; i < n + 2; i += kRedThreads) {
         const int64_t t = i0 + i - 1;
-        s_id[i] = t >= 0 && t < a.T ? __ldg(ids + t) : kNone;
-        if (i >= 1 && i <= n) s_pos[i - 1] = __ldg(pos + t);
+        s_id[i] = t >= 0 && t < a.T ? __ldcg(ids + t) : kNone;
+        if (i >= 1 && i <= n) s_pos[i - 1] = __ldcg(pos + t);
     }
     __syncthreads();
     const int64_t c = int64_t(blockIdx.y) * kRedCols + threadIdx.x * 8;
-    if (c >= a.H || s_id[1] >= a.V) return;         // keys ascend: V at the first token means V throughout
+    const uint32_t V = static_cast<uint32_t>(a.V), first = s_id[1], before = s_id[0];
+    if (c >= a.H || first >= V) return;              // keys ascend: V at the first token means V throughout
     float acc[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-    bool from_first = true;                          // the current run starts at the chunk's first token
-    for (int i = 0; i < n; i += 8) {
-        uint4 r[8][2];
+    for (int i = 0; i < n; i += kBatch) {
+        Raw<kDyBf16, 8> r[kBatch];
+        Raw<kDeBf16, 8> old[kBatch];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (i + u < n && s_id[i + u + 1] < a.V) load_dy(a, s_pos[i + u], c, r[u]);
+        for (int u = 0; u < kBatch; ++u) {
+            old[u].zero();
+            if (i + u >= n) continue;
+            const uint32_t id = s_id[i + u + 1];
+            if (id >= V) continue;
+            r[u].load(a.dY, int64_t(s_pos[i + u]) * a.H + c);
+            if (kAdd && s_id[i + u + 2] != id && !(id == first && before == id)) old[u].load(a.dE, int64_t(id) * a.H + c);
+        }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (i + u >= n || s_id[i + u + 1] >= a.V) break;
-            add_dy(a, r[u], acc);
+        for (int u = 0; u < kBatch; ++u) {
+            if (i + u >= n) break;
             const uint32_t id = s_id[i + u + 1], next = s_id[i + u + 2];
+            if (id >= V) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += r[u].at(j);
             if (next == id && i + u + 1 < n) continue;
             // the run ends in this chunk, or the chunk ends in it
-            if (next == id || (from_first && s_id[0] == id)) {
-                float4 *dst = reinterpret_cast<float4 *>(a.part + (2 * ch + (from_first ? 0 : 1)) * a.H + c);
+            if (next == id || (id == first && before == id)) {
+                float4 *dst = reinterpret_cast<float4 *>(a.part + (2 * ch + (id == first ? 0 : 1)) * a.H + c);
                 dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
                 dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
             } else {
-                write_row<8>(a, id, c, acc);
+                write_row<kDeBf16, 8>(a, id, c, acc, old[u]);
             }
-            from_first = false;
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = 0.f;
         }
@@ -447,22 +492,42 @@ constexpr int kLongJoin = 32;
 __device__ __forceinline__ void add4(float4 &s, const float4 x) {
     s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
 }
+__device__ __forceinline__ float4 load_part(const GradArgs &a, int64_t slot, int64_t c) {
+    return __ldcg(reinterpret_cast<const float4 *>(a.part + slot * a.H + c));
+}
 // sum of the first-run partials of chunks [lo, hi), columns c .. c + 3, on top of s
 __device__ __forceinline__ float4 sum_firsts(const GradArgs &a, float4 s, int64_t lo, int64_t hi, int64_t c) {
     for (; lo + 8 <= hi; lo += 8) {
         float4 x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = __ldcg(reinterpret_cast<const float4 *>(a.part + 2 * (lo + u) * a.H + c));
+        for (int u = 0; u < 8; ++u) x[u] = load_part(a, 2 * (lo + u), c);
 #pragma unroll
         for (int u = 0; u < 8; ++u) add4(s, x[u]);
     }
-    for (; lo < hi; ++lo) add4(s, __ldcg(reinterpret_cast<const float4 *>(a.part + 2 * lo * a.H + c)));
+    for (; lo < hi; ++lo) add4(s, load_part(a, 2 * lo, c));
     return s;
 }
+// one past the last chunk that starts with id, given that chunk lo does: 32 chunks at a time over the
+// whole warp, the next 32 first (few ids go further), then 32 places spread over what is left
+__device__ __forceinline__ int64_t end_of_id(const GradArgs &a, const uint32_t *ids, uint32_t id, int64_t lo, int lane) {
+    int64_t hi = a.nchunks, stride = 1;
+    while (lo + 1 < hi) {                      // chunk lo starts with id, chunk hi does not (or is the end)
+        const int64_t k = lo + (lane + 1) * stride;
+        const bool same = k < hi && __ldcg(ids + k * a.chunk) == id;
+        const int n = __popc(__ballot_sync(0xffffffffu, same));      // sorted: the first n places hold id
+        lo += n * stride;
+        hi = min(hi, n < 32 ? lo + stride : hi);
+        stride = max(int64_t(1), (hi - lo + 31) / 32);
+    }
+    return lo + 1;
+}
+template <bool kDeBf16>
 __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradArgs a) {
     __shared__ int64_t s_end[kJoinWarps];
     __shared__ uint32_t s_id[kJoinWarps], s_slot[kJoinWarps];
     __shared__ float4 s_part[kJoinWarps][32];
+    pdl_launch_dependents();
+    pdl_wait();
     const uint32_t *ids = a.key[a.passes & 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t c = int64_t(blockIdx.y) * kJoinCols + lane * 4;
@@ -471,25 +536,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradA
     uint32_t id = 0, slot = 0;
     if (ch + 1 < a.nchunks) {
         const int64_t i0 = ch * a.chunk;
-        id = __ldg(ids + i0 + a.chunk - 1);
-        if (id < a.V && __ldg(ids + i0 + a.chunk) == id) {
-            const bool whole = __ldg(ids + i0) == id;             // one id throughout the chunk
-            if (!(whole && ch > 0 && __ldg(ids + i0 - 1) == id)) {
-                slot = whole ? 0 : 1;
-                int64_t lo = ch + 1, hi = a.nchunks;              // chunk lo starts with id; find the first that does not
-                while (hi - lo > 1) {
-                    const int64_t mid = (lo + hi) / 2;
-                    if (__ldg(ids + mid * a.chunk) == id) lo = mid;
-                    else hi = mid;
-                }
-                end = lo + 1;
-            }
+        id = __ldcg(ids + i0 + a.chunk - 1);
+        const uint32_t after = __ldcg(ids + i0 + a.chunk), first = __ldcg(ids + i0);
+        const uint32_t before = ch > 0 ? __ldcg(ids + i0 - 1) : 0xFFFFFFFFu;
+        // first == id: one id throughout the chunk; if it also ends the chunk before, that one (or one before) owns it
+        if (id < a.V && after == id && !(first == id && before == id)) {
+            slot = first == id ? 0 : 1;
+            end = end_of_id(a, ids, id, ch + 1, lane);
         }
     }
+    Raw<kDeBf16, 4> old;
+    old.zero();
     if (end && end - ch <= kLongJoin && c < a.H) {
-        float4 s = __ldcg(reinterpret_cast<const float4 *>(a.part + (2 * ch + slot) * a.H + c));
-        s = sum_firsts(a, s, ch + 1, end, c);
-        write_row<4>(a, id, c, reinterpret_cast<const float *>(&s));
+        if (a.accumulate) old.load(a.dE, int64_t(id) * a.H + c);
+        const float4 s = sum_firsts(a, load_part(a, 2 * ch + slot, c), ch + 1, end, c);
+        write_row<kDeBf16, 4>(a, id, c, reinterpret_cast<const float *>(&s), old);
     }
     if (lane == 0) {
         s_end[warp] = end && end - ch > kLongJoin ? end : 0;
@@ -502,7 +563,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradA
         const int64_t lo = ch - warp + w + 1, n = s_end[w] - lo;  // first-run partials of chunks [lo, lo + n)
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c < a.H) {
-            if (warp == 0) s = __ldcg(reinterpret_cast<const float4 *>(a.part + (2 * (lo - 1) + s_slot[w]) * a.H + c));
+            if (warp == 0) s = load_part(a, 2 * (lo - 1) + s_slot[w], c);
+            if (warp == 0 && a.accumulate) old.load(a.dE, int64_t(s_id[w]) * a.H + c);
             s = sum_firsts(a, s, lo + n * warp / kJoinWarps, lo + n * (warp + 1) / kJoinWarps, c);
         }
         s_part[warp][lane] = s;
@@ -510,7 +572,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradA
         if (warp == 0 && c < a.H) {
 #pragma unroll
             for (int i = 1; i < kJoinWarps; ++i) add4(s, s_part[i][lane]);
-            write_row<4>(a, s_id[w], c, reinterpret_cast<const float *>(&s));
+            write_row<kDeBf16, 4>(a, s_id[w], c, reinterpret_cast<const float *>(&s), old);
         }
         __syncthreads();
     }

@@ -2,6 +2,7 @@
 // validation, error reporting and TMA tensor-map construction.
 #pragma once
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -218,15 +219,19 @@ static qlora_status make_tmap_code_chunks(CUtensorMap *map, const void *codes, u
 }
 
 // ------------------------------------------------------------------ device checks
+// (A device's answer does not change: devices that passed are remembered, one bit each.)
 static qlora_status require_sm100() {
+    static std::atomic<uint64_t> passed{0};
     int dev = 0;
     QL_TRY(cuda_check(cudaGetDevice(&dev), "cudaGetDevice"));
+    if (dev >= 0 && dev < 64 && (passed.load(std::memory_order_relaxed) >> dev) & 1) return QLORA_OK;
     int major = 0, minor = 0;
     QL_TRY(cuda_check(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev), "cc major"));
     QL_TRY(cuda_check(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev), "cc minor"));
     if (major != 10 || minor != 0)
         return fail(QLORA_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_100a only", dev,
                     major, minor);
+    if (dev >= 0 && dev < 64) passed.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     return QLORA_OK;
 }
 

@@ -166,53 +166,64 @@ __device__ __forceinline__ void decode8(const uint32_t *c, float d, float *x) {
         x[i] = __fmul_rn(__fmul_rn(k, fabsf(k)), d);
     }
 }
-// Codes of a lane's 8 values x (signed m, or sqrt(v) >= 0) and the block's step d.  The
-// candidate is the square root's nearest integer; only where the root lies within 2e-4 of a
-// half (the approximate root is good to 4e-5 there) is it checked against the exact border.
+// roots to 2^-23: kFtz takes inputs below 2^-126 as 0
+template <bool kFtz>
+__device__ __forceinline__ float sqrt_approx(float x) {
+    float r;
+    if (kFtz) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    else asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// the larger magnitude as bits: an infinity is above every finite value, a NaN above that
+__device__ __forceinline__ uint32_t max_bits(uint32_t a, float x) { return max(a, __float_as_uint(x) & 0x7FFFFFFFu); }
+
+// A block's step d = RN(a / top^2) from the bits of its largest magnitude a, and RN(1 / d)
+__device__ __forceinline__ void block_step(uint32_t a_bits, float top2, float &d, float &inv) {
+    d = __fdiv_rn(__uint_as_float(a_bits), top2);
+    inv = __frcp_rn(d);
+    if (d < 1.17549435e-38f) d = 0.f, inv = 0.f;
+    if (a_bits >= 0x7F800000u) d = __uint_as_float(0x7FC00000u), inv = 0.f;
+}
+
+// Codes of a lane's 8 values given inv = RN(1 / d).  kSigned: x holds m.  Otherwise x holds v, of
+// which y = RN(RN(sqrt(v)) inv) is coded, and w its approximate root.  The candidate is the
+// nearest integer to an approximate sqrt(y - 1/4), good to 1e-4 for k up to 255 (relative errors of
+// 2^-22 each in root and product); only where that root lies within 2e-4 of a half is y formed
+// exactly and the candidate checked against the borders.
+constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer in the low mantissa bits
 template <bool kSigned>
-__device__ __forceinline__ float encode8(const float *x, uint32_t *c) {
-    constexpr float kTop2 = kSigned ? float(kTopM * kTopM) : float(kTopW * kTopW);
-    uint32_t a = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    a = __reduce_max_sync(0xffffffffu, a);
-    float d = 0.f, inv = 0.f;
-    if (a >= 0x7F800000u) {
-        d = __uint_as_float(0x7FC00000u);
-    } else {
-        d = __fdiv_rn(__uint_as_float(a), kTop2);
-        if (d < 1.17549435e-38f) d = 0.f;
-        else inv = __frcp_rn(d);
-    }
-    constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer in the low bits
-    float y[8], k[8], off = 0.f;
+__device__ __forceinline__ void encode8(const float *x, const float *w, float inv, uint32_t *c) {
+    float t[8], off = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        y[i] = __fmul_rn(fabsf(x[i]), inv);
-        float r;
-        asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(__fsub_rn(y[i], 0.25f), 0.f)));
-        k[i] = __fsub_rn(__fadd_rn(r, kMagic), kMagic);
-        off = fmaxf(off, fabsf(r - k[i]));
+        const float r = sqrt_approx<true>(fmaxf(fmaf(kSigned ? fabsf(x[i]) : w[i], inv, -0.25f), 0.f));
+        t[i] = __fadd_rn(r, kMagic);
+        off = fmaxf(off, fabsf(r - __fsub_rn(t[i], kMagic)));
     }
     if (off > 0.4998f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            const float y = __fmul_rn(kSigned ? fabsf(x[i]) : __fsqrt_rn(x[i]), inv), k = __fsub_rn(t[i], kMagic);
             // k^2 + k + 1/2 is exact: at most 17 significant bits
-            if (y[i] > __fmaf_rn(k[i], k[i], k[i]) + 0.5f) k[i] += 1.f;
-            else if (k[i] > 0.f && y[i] <= __fmaf_rn(k[i], k[i], -k[i]) + 0.5f) k[i] -= 1.f;
+            if (y > __fmaf_rn(k, k, k) + 0.5f) t[i] += 1.f;
+            else if (k > 0.f && y <= __fmaf_rn(k, k, -k) + 0.5f) t[i] -= 1.f;
         }
+    }
+    if (kSigned) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = __fadd_rn(copysignf(__fsub_rn(t[i], kMagic), x[i]), kMagic);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        uint32_t b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float s = kSigned ? copysignf(k[4 * h + j], x[4 * h + j]) : k[4 * h + j];
-            b[j] = __float_as_uint(__fadd_rn(s, kMagic));
-        }
-        c[h] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        const uint32_t lo = __byte_perm(__float_as_uint(t[4 * h]), __float_as_uint(t[4 * h + 1]), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(t[4 * h + 2]), __float_as_uint(t[4 * h + 3]), 0x0040);
+        c[h] = __byte_perm(lo, hi, 0x5410);
     }
-    return d;
 }
 
 struct StepArgs {
@@ -221,9 +232,10 @@ struct StepArgs {
     const float *coef;         // clip coefficient on the device, or NULL
     const float *lr_dev;       // learning rate on the device, or NULL
     int64_t *step_dev;         // number of steps taken, or NULL
-    double beta1, beta2;
+    double beta1, beta2, eps;
     int64_t nchunks;
-    float lr, b1, w1, b2, w2, eps, ibc1, ibc2;   // w = 1 - b; ibc1 = 1/(1 - b1^t), ibc2 = 1/sqrt(1 - b2^t)
+    float lr, b1, w1, b2, w2;  // w = 1 - b
+    float ds, de;              // (1 - b1^t) / sqrt(1 - b2^t) and (1 - b1^t) eps
 };
 
 // b^t by squaring (t >= 1): at most 2 log2(t) products, each rounded in double
@@ -234,103 +246,143 @@ __device__ __forceinline__ double pow_int(double b, int64_t t) {
     return r;
 }
 
-template <bool kState8, bool kFull>
-__device__ __forceinline__ void step_block(const StepArgs &a, uint64_t P, uint64_t copy, uint64_t G, uint64_t Mo,
-                                           uint64_t Vo, uint64_t DM, uint64_t DV, uint32_t flags, float lr, float decay,
-                                           float coef, float ibc1, float ibc2, int64_t i0, int rem, int lane) {
-    float g[8], p[8], m[8], v[8];
+// A chunk's addresses and settings, the same in every lane.
+struct View {
+    uint64_t p, copy, g, m, v, dm, dv;
+    int n;
+    uint32_t flags;
+    float lr, decay;
+};
+__device__ __forceinline__ View view_of(uint32_t word, float lr) {
+    View c;
+    c.p = word64(word, 0), c.copy = word64(word, 2), c.g = word64(word, 4), c.m = word64(word, 6);
+    c.v = word64(word, 8), c.dm = word64(word, 10), c.dv = word64(word, 12);
+    c.n = static_cast<int>(word32(word, 14));
+    c.flags = word32(word, 15);
+    c.lr = lr * __uint_as_float(word32(word, 16));
+    c.decay = __uint_as_float(word32(word, 17));
+    return c;
+}
+// The step's scalars: denominators are (sqrt(v) ibc2 + eps) bc1 = sqrt(v) ds + de.
+struct Scalars {
+    float coef, ds, de;
+};
+
+// One block of 256 (kFull) or the rem < 256 last elements of a tensor.
+template <bool kState8, bool kPBf16, bool kGBf16, bool kFull>
+__device__ __forceinline__ void step_block(const StepArgs &a, const View &c, const Scalars &s, int64_t i0, int rem, int lane) {
+    float g[8], p[8], m[8], v[8], w[8];
     uint32_t cm[2], cv[2];
     float dm = 0.f, dv = 0.f;
-    load8<kFull>(G, (flags & kGradBf16) != 0, i0, rem, lane, g);
-    load8<kFull>(P, (flags & kParamBf16) != 0, i0, rem, lane, p);
     if (kState8) {
-        load_codes<kFull>(Mo, i0, rem, lane, cm);
-        load_codes<kFull>(Vo, i0, rem, lane, cv);
-        dm = reinterpret_cast<const float *>(DM)[i0 / kBlock];
-        dv = reinterpret_cast<const float *>(DV)[i0 / kBlock];
+        load_codes<kFull>(c.m, i0, rem, lane, cm);
+        load_codes<kFull>(c.v, i0, rem, lane, cv);
+        dm = reinterpret_cast<const float *>(c.dm)[i0 / kBlock];
+        dv = reinterpret_cast<const float *>(c.dv)[i0 / kBlock];
+    } else {
+        load8<kFull>(c.m, false, i0, rem, lane, m);
+        load8<kFull>(c.v, false, i0, rem, lane, v);
+    }
+    load8<kFull>(c.g, kGBf16, i0, rem, lane, g);
+    load8<kFull>(c.p, kPBf16, i0, rem, lane, p);
+    if (kState8) {
         decode8<true>(cm, dm, m);
         decode8<false>(cv, dv, v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], v[i]);
-    } else {
-        load8<kFull>(Mo, false, i0, rem, lane, m);
-        load8<kFull>(Vo, false, i0, rem, lane, v);
     }
-    float w[8];
+    uint32_t am = 0, av = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float gi = a.coef ? __fmul_rn(g[i], coef) : g[i];
+        const float gi = __fmul_rn(g[i], s.coef);
         m[i] = __fadd_rn(__fmul_rn(a.b1, m[i]), __fmul_rn(a.w1, gi));
         v[i] = __fadd_rn(__fmul_rn(a.b2, v[i]), __fmul_rn(a.w2, __fmul_rn(gi, gi)));
-        w[i] = __fsqrt_rn(v[i]);
-        const float u = __fdividef(m[i] * ibc1, fmaf(w[i], ibc2, a.eps));
-        p[i] = fmaf(-lr, fmaf(decay, p[i], u), p[i]);
-    }
-    store8<kFull>(P, (flags & kParamBf16) != 0, i0, rem, lane, p);
-    if (copy) store8<kFull>(copy, true, i0, rem, lane, p);
-    if (kState8) {
-        if (!kFull) {   // places past the tensor's end take no part in the block's largest value
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if ((i >> 2) * 128 + lane * 4 + (i & 3) >= rem) m[i] = w[i] = 0.f;
+        w[i] = sqrt_approx<false>(v[i]);
+        p[i] = fmaf(-c.lr, fmaf(c.decay, p[i], m[i] * rcp_approx(fmaf(w[i], s.ds, s.de))), p[i]);
+        if (kState8 && (kFull || (i >> 2) * 128 + lane * 4 + (i & 3) < rem)) {
+            am = max_bits(am, m[i]);
+            av = max_bits(av, v[i]);
         }
-        dm = encode8<true>(m, cm);
-        dv = encode8<false>(w, cv);
-        store_codes<kFull>(Mo, i0, rem, lane, cm);
-        store_codes<kFull>(Vo, i0, rem, lane, cv);
+    }
+    store8<kFull>(c.p, kPBf16, i0, rem, lane, p);
+    if (!kPBf16 && c.copy) store8<kFull>(c.copy, true, i0, rem, lane, p);
+    if (kState8) {
+        am = __reduce_max_sync(0xffffffffu, am);
+        av = __reduce_max_sync(0xffffffffu, av);
+        // the root is monotonic, so the largest root is the root of the largest v; even lanes work out m's
+        // step and odd lanes sqrt(v)'s
+        const bool odd = lane & 1;
+        if (av < 0x7F800000u) av = __float_as_uint(__fsqrt_rn(__uint_as_float(av)));
+        float d, inv;
+        block_step(odd ? av : am, odd ? float(kTopW * kTopW) : float(kTopM * kTopM), d, inv);
+        dm = __shfl_sync(0xffffffffu, d, 0);
+        dv = __shfl_sync(0xffffffffu, d, 1);
+        encode8<true>(m, nullptr, __shfl_sync(0xffffffffu, inv, 0), cm);
+        encode8<false>(v, w, __shfl_sync(0xffffffffu, inv, 1), cv);
+        store_codes<kFull>(c.m, i0, rem, lane, cm);
+        store_codes<kFull>(c.v, i0, rem, lane, cv);
         if (lane == 0) {
-            reinterpret_cast<float *>(DM)[i0 / kBlock] = dm;
-            reinterpret_cast<float *>(DV)[i0 / kBlock] = dv;
+            reinterpret_cast<float *>(c.dm)[i0 / kBlock] = dm;
+            reinterpret_cast<float *>(c.dv)[i0 / kBlock] = dv;
         }
     } else {
-        store8<kFull>(Mo, false, i0, rem, lane, m);
-        store8<kFull>(Vo, false, i0, rem, lane, v);
+        store8<kFull>(c.m, false, i0, rem, lane, m);
+        store8<kFull>(c.v, false, i0, rem, lane, v);
+    }
+}
+template <bool kState8, bool kPBf16, bool kGBf16>
+__device__ __forceinline__ void step_chunk(const StepArgs &a, const View &c, const Scalars &s, int lane) {
+    int i0 = 0;
+    for (; i0 + kBlock <= c.n; i0 += kBlock) step_block<kState8, kPBf16, kGBf16, true>(a, c, s, i0, kBlock, lane);
+    if (i0 < c.n) step_block<kState8, kPBf16, kGBf16, false>(a, c, s, i0, c.n - i0, lane);
+}
+template <bool kState8>
+__device__ __forceinline__ void step_types(const StepArgs &a, const View &c, const Scalars &s, int lane) {
+    switch (c.flags & (kParamBf16 | kGradBf16)) {
+        case 0: step_chunk<kState8, false, false>(a, c, s, lane); break;
+        case kParamBf16: step_chunk<kState8, true, false>(a, c, s, lane); break;
+        case kGradBf16: step_chunk<kState8, false, true>(a, c, s, lane); break;
+        default: step_chunk<kState8, true, true>(a, c, s, lane);
     }
 }
 
 // A warp takes every (warps of the grid)-th chunk, with the next chunk's 80 bytes already on
-// their way; no barrier and no shared memory in the loop.
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const StepArgs a) {
+// their way; no barrier and no shared memory in the loop.  kKinds: the states the plan holds,
+// kKind32 | kKind8.
+enum { kKind32 = 1, kKind8 = 2 };
+constexpr int kCtas32 = 4, kCtas8 = 3;      // CTAs per SM that the registers are capped for
+template <int kKinds>
+__global__ void __launch_bounds__(kThreads, kKinds == kKind32 ? kCtas32 : kCtas8) adamw_kernel(const StepArgs a) {
     __shared__ float s_bc[2];
     const int lane = threadIdx.x & 31;
     const int64_t nw = int64_t(gridDim.x) * kWarps;
-    int64_t c = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    uint32_t word = c < a.nchunks ? chunk_word(a.chunks, c, lane) : 0u;
-    const float coef = a.coef ? __ldg(a.coef) : 1.f;
-    if (!isfinite(coef)) return;          // the gradients held an infinity or a NaN: nothing changes
-    const float lr = a.lr_dev ? __ldg(a.lr_dev) : a.lr;
-    float ibc1 = a.ibc1, ibc2 = a.ibc2;
+    int64_t i = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    // the chunk list was complete when the plan's call returned: it may be read before the wait
+    uint32_t word = i < a.nchunks ? chunk_word(a.chunks, i, lane) : 0u;
+    pdl_launch_dependents();
+    pdl_wait();
+    Scalars s;
+    s.coef = a.coef ? __ldcg(a.coef) : 1.f;          // a product with 1 changes nothing
+    if (!isfinite(s.coef)) return;                   // the gradients held an infinity or a NaN: nothing changes
+    const float lr = a.lr_dev ? __ldcg(a.lr_dev) : a.lr;
+    s.ds = a.ds;
+    s.de = a.de;
     if (a.step_dev) {
         if (threadIdx.x == 0) {
             const int64_t t = *a.step_dev + 1;
-            s_bc[0] = static_cast<float>(1.0 / (1.0 - pow_int(a.beta1, t)));
-            s_bc[1] = static_cast<float>(1.0 / sqrt(1.0 - pow_int(a.beta2, t)));
+            const double bc1 = 1.0 - pow_int(a.beta1, t);
+            s_bc[0] = static_cast<float>(bc1 / sqrt(1.0 - pow_int(a.beta2, t)));
+            s_bc[1] = static_cast<float>(bc1 * a.eps);
         }
         __syncthreads();
-        ibc1 = s_bc[0];
-        ibc2 = s_bc[1];
+        s.ds = s_bc[0];
+        s.de = s_bc[1];
     }
-    for (; c < a.nchunks; c += nw) {
-        const uint64_t P = word64(word, 0), copy = word64(word, 2), G = word64(word, 4), Mo = word64(word, 6),
-                       Vo = word64(word, 8), DM = word64(word, 10), DV = word64(word, 12);
-        const int n = static_cast<int>(word32(word, 14));
-        const uint32_t flags = word32(word, 15);
-        const float lrc = lr * __uint_as_float(word32(word, 16)), decay = __uint_as_float(word32(word, 17));
-        if (c + nw < a.nchunks) word = chunk_word(a.chunks, c + nw, lane);
-        for (int i0 = 0; i0 < n; i0 += kBlock) {
-            const int rem = n - i0;
-            if (flags & kState8) {
-                if (rem >= kBlock)
-                    step_block<true, true>(a, P, copy, G, Mo, Vo, DM, DV, flags, lrc, decay, coef, ibc1, ibc2, i0, rem, lane);
-                else
-                    step_block<true, false>(a, P, copy, G, Mo, Vo, DM, DV, flags, lrc, decay, coef, ibc1, ibc2, i0, rem, lane);
-            } else {
-                if (rem >= kBlock)
-                    step_block<false, true>(a, P, copy, G, Mo, Vo, DM, DV, flags, lrc, decay, coef, ibc1, ibc2, i0, rem, lane);
-                else
-                    step_block<false, false>(a, P, copy, G, Mo, Vo, DM, DV, flags, lrc, decay, coef, ibc1, ibc2, i0, rem, lane);
-            }
-        }
+    for (; i < a.nchunks; i += nw) {
+        const View c = view_of(word, lr);
+        if (i + nw < a.nchunks) word = chunk_word(a.chunks, i + nw, lane);
+        if (kKinds == kKind32 || (kKinds != kKind8 && !(c.flags & kState8))) step_types<false>(a, c, s, lane);
+        else step_types<true>(a, c, s, lane);
     }
     if (a.step_dev) {
         // the last CTA to get here counts the step: every CTA has read the counter by then
@@ -357,6 +409,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Chunk *chunks
     const int64_t nw = int64_t(gridDim.x) * kWarps;
     int64_t c = int64_t(blockIdx.x) * kWarps + warp;
     uint32_t word = c < nchunks ? chunk_word(chunks, c, lane) : 0u;
+    pdl_launch_dependents();
+    pdl_wait();
     double sum = 0.0;
     for (; c < nchunks; c += nw) {
         const uint64_t G = word64(word, 4);
@@ -407,33 +461,41 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Chunk *chunks
 // 8-bit state from float32 moments, and back.  kSecond: x is the second moment v, coded by
 // its root, and comes back as the square of the decoded root.
 template <bool kSecond>
-__global__ void __launch_bounds__(kThreads) adam8_encode_kernel(const float *__restrict__ x, uint8_t *__restrict__ codes,
-                                                                float *__restrict__ steps, int64_t n) {
+__global__ void __launch_bounds__(kThreads) adam8_encode_kernel(const float *x, uint8_t *codes, float *steps, int64_t n) {
     const int lane = threadIdx.x & 31;
     const int64_t nblk = (n + kBlock - 1) / kBlock;
+    pdl_launch_dependents();
+    pdl_wait();
     for (int64_t b = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); b < nblk; b += int64_t(gridDim.x) * kWarps) {
         const int rem = static_cast<int>(n - b * kBlock < kBlock ? n - b * kBlock : kBlock);
         const uint64_t src = reinterpret_cast<uint64_t>(x), dst = reinterpret_cast<uint64_t>(codes);
         float f[8];
         if (rem == kBlock) load8<true>(src, false, b * kBlock, rem, lane, f);
         else load8<false>(src, false, b * kBlock, rem, lane, f);
-        if (kSecond) {
+        uint32_t c[2], top = 0;
+        float w[8], d, inv;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __fsqrt_rn(f[i]);
+        for (int i = 0; i < 8; ++i) {
+            if (kSecond) f[i] += 0.f;                       // -0 becomes 0
+            // a negative v has no root: its sign bit puts it above infinity here, with the NaNs
+            top = max(top, __float_as_uint(f[i]) & (kSecond ? 0xFFFFFFFFu : 0x7FFFFFFFu));
+            w[i] = sqrt_approx<false>(f[i]);
         }
-        uint32_t c[2];
-        const float d = encode8<!kSecond>(f, c);
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (kSecond && top < 0x7F800000u) top = __float_as_uint(__fsqrt_rn(__uint_as_float(top)));
+        block_step(top, kSecond ? float(kTopW * kTopW) : float(kTopM * kTopM), d, inv);
+        encode8<!kSecond>(f, w, inv, c);
         if (rem == kBlock) store_codes<true>(dst, b * kBlock, rem, lane, c);
         else store_codes<false>(dst, b * kBlock, rem, lane, c);
         if (lane == 0) steps[b] = d;
     }
 }
 template <bool kSecond>
-__global__ void __launch_bounds__(kThreads) adam8_decode_kernel(const uint8_t *__restrict__ codes,
-                                                                const float *__restrict__ steps, float *__restrict__ x,
-                                                                int64_t n) {
+__global__ void __launch_bounds__(kThreads) adam8_decode_kernel(const uint8_t *codes, const float *steps, float *x, int64_t n) {
     const int lane = threadIdx.x & 31;
     const int64_t nblk = (n + kBlock - 1) / kBlock;
+    pdl_launch_dependents();
+    pdl_wait();
     for (int64_t b = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); b < nblk; b += int64_t(gridDim.x) * kWarps) {
         const int rem = static_cast<int>(n - b * kBlock < kBlock ? n - b * kBlock : kBlock);
         const uint64_t src = reinterpret_cast<uint64_t>(codes), dst = reinterpret_cast<uint64_t>(x);
@@ -441,7 +503,7 @@ __global__ void __launch_bounds__(kThreads) adam8_decode_kernel(const uint8_t *_
         if (rem == kBlock) load_codes<true>(src, b * kBlock, rem, lane, c);
         else load_codes<false>(src, b * kBlock, rem, lane, c);
         float f[8];
-        decode8<!kSecond>(c, __ldg(steps + b), f);
+        decode8<!kSecond>(c, __ldcg(steps + b), f);
         if (kSecond) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], f[i]);

@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
+#include <utility>
 
 #include "host_common.cuh"
 #include "ptx.cuh"
@@ -131,6 +132,24 @@ qlora_status set_smem(K kernel, int bytes) {
     if (slot < 0 && ndone < 256) slot = ndone++;
     if (slot >= 0) done[slot] = SmemSetting{key, dev, bytes};
     return QLORA_OK;
+}
+
+// Launch with programmatic stream serialization: the kernel may start while the preceding one still
+// runs, and calls pdl_wait() before it touches memory that others write.
+template <typename... P, typename... A>
+qlora_status launch_pdl(const char *what, void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st,
+                        A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cuda_check(cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...), what);
 }
 
 qlora_status launch_check(const char *what) { return cuda_check(cudaGetLastError(), what); }
@@ -977,9 +996,11 @@ static qlora_status launch_embed_fwd(emb::FwdArgs &a, const void *ids, int ids_b
     if (T == 0) return QLORA_OK;
     if (!Y) return fail(QLORA_ERR_ARG, "Y is NULL");
     if (!aligned16(Y)) return fail(QLORA_ERR_ALIGN, "Y must be 16-byte aligned");
-    a.segs = static_cast<int>(ceil_div(H, emb::kRun));
-    const int64_t grid = ceil_div(T * a.segs, emb::kFwdThreads / 32);
-    if (grid > INT32_MAX) return fail(QLORA_ERR_SHAPE, "T x H is too large for one call");
+    const int64_t segs = ceil_div(H, emb::kRun);
+    a.seg_shift = 0;
+    while ((1 << a.seg_shift) < segs && (2 << a.seg_shift) <= emb::kFwdWarps) ++a.seg_shift;
+    const int64_t gx = ceil_div(T, emb::kFwdWarps >> a.seg_shift), gy = ceil_div(segs, int64_t(1) << a.seg_shift);
+    if (gy > 65535) return fail(QLORA_ERR_SHAPE, "the row length (%lld) is too large", (long long)H);
     QL_TRY(require_sm100());
     a.ids = emb::Ids{ids, ids_bytes == 8};
     a.out = Y;
@@ -987,10 +1008,10 @@ static qlora_status launch_embed_fwd(emb::FwdArgs &a, const void *ids, int ids_b
     a.V = V;
     a.H = H;
     a.scale = scale;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (y_is_bf16) emb::embed_fwd_kernel<kTable, true><<<static_cast<unsigned>(grid), emb::kFwdThreads, 0, st>>>(a);
-    else emb::embed_fwd_kernel<kTable, false><<<static_cast<unsigned>(grid), emb::kFwdThreads, 0, st>>>(a);
-    return launch_check("embed_fwd_kernel launch");
+    return launch_pdl("embed_fwd_kernel launch",
+                      y_is_bf16 ? emb::embed_fwd_kernel<kTable, true> : emb::embed_fwd_kernel<kTable, false>,
+                      dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), emb::kFwdThreads, 0,
+                      static_cast<cudaStream_t>(stream), a);
 }
 
 extern "C" {
@@ -1081,21 +1102,25 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
     if (jtiles > 65535) return fail(QLORA_ERR_SHAPE, "H (%lld) must be at most %d", (long long)H, 65535 * emb::kJoinCols);
     QL_TRY(require_sm100());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // one cluster sorts; when the whole table is written, a cluster per eight other SMs zeroes rows meanwhile
-    const int zero_clusters = accumulate ? 0 : std::max(1, sm_count() / emb::kSortCtas - 1);
-    QL_TRY(set_smem(emb::embed_sort_kernel, emb::kSortSmem));
-    emb::embed_sort_kernel<<<static_cast<unsigned>(emb::kSortCtas * (1 + zero_clusters)), emb::kSortThreads,
-                             emb::kSortSmem, st>>>(a);
-    QL_TRY(launch_check("embed_sort_kernel launch"));
-    if (T == 0) return QLORA_OK;
-    emb::embed_reduce_kernel<<<dim3(static_cast<unsigned>(a.nchunks), static_cast<unsigned>(tiles)), emb::kRedThreads, 0,
-                               st>>>(a);
-    QL_TRY(launch_check("embed_reduce_kernel launch"));
-    if (a.nchunks > 1) {
-        emb::embed_join_kernel<<<dim3(static_cast<unsigned>(ceil_div(a.nchunks - 1, emb::kJoinWarps)),
-                                      static_cast<unsigned>(jtiles)), emb::kJoinWarps * 32, 0, st>>>(a);
-        QL_TRY(launch_check("embed_join_kernel launch"));
+    if (T > 0) {
+        QL_TRY(set_smem(emb::embed_sort_kernel, emb::kSortSmem));
+        QL_TRY(launch_pdl("embed_sort_kernel launch", emb::embed_sort_kernel, dim3(emb::kSortCtas), emb::kSortThreads,
+                          emb::kSortSmem, st, a));
+        void (*const reduce[8])(emb::GradArgs) = {
+            emb::embed_reduce_kernel<false, false, false>, emb::embed_reduce_kernel<false, false, true>,
+            emb::embed_reduce_kernel<false, true, false>,  emb::embed_reduce_kernel<false, true, true>,
+            emb::embed_reduce_kernel<true, false, false>,  emb::embed_reduce_kernel<true, false, true>,
+            emb::embed_reduce_kernel<true, true, false>,   emb::embed_reduce_kernel<true, true, true>};
+        QL_TRY(launch_pdl("embed_reduce_kernel launch", reduce[4 * dy_is_bf16 + 2 * de_is_bf16 + accumulate],
+                          dim3(static_cast<unsigned>(a.nchunks), static_cast<unsigned>(tiles)), emb::kRedThreads, 0, st, a));
+        if (a.nchunks > 1)
+            QL_TRY(launch_pdl("embed_join_kernel launch", de_is_bf16 ? emb::embed_join_kernel<true> : emb::embed_join_kernel<false>,
+                              dim3(static_cast<unsigned>(ceil_div(a.nchunks - 1, emb::kJoinWarps)), static_cast<unsigned>(jtiles)),
+                              emb::kJoinWarps * 32, 0, st, a));
     }
+    if (!accumulate)
+        QL_TRY(launch_pdl("embed_zero_kernel launch", emb::embed_zero_kernel, dim3(static_cast<unsigned>(2 * sm_count())),
+                          emb::kZeroThreads, 0, st, a, int(T == 0)));
     return QLORA_OK;
 }
 
@@ -1105,11 +1130,13 @@ static_assert(sizeof(qlora_adamw_tensor) == 80 && offsetof(qlora_adamw_tensor, f
 static_assert(sizeof(qlora_adamw_plan) == 48, "ABI layout");
 constexpr int32_t kOptFlags = QLORA_OPT_PARAM_BF16 | QLORA_OPT_GRAD_BF16 | QLORA_OPT_STATE_8BIT | QLORA_OPT_GRAD_ONLY;
 constexpr int32_t kPlanMagic = 0x51504c4e;
+constexpr int32_t kPlanGradOnly = 4;   // beside optim::kKind32 and kKind8 in a plan's kinds
 
-// Elements of a plan's chunk for `numel` in all: the largest multiple of 256 from 256 to 2048 that still
-// gives every warp of the device (64 per SM) a chunk.
+// Elements of a plan's chunk for `numel` in all: the largest multiple of 256 from 256 to 1024 that still
+// gives every warp of the device (64 per SM) a chunk.  A chunk's 80 bytes are 0.3 to 0.8 % of the bytes
+// of 1024 elements; the last round of a large plan's chunks leaves 1 to 2 % of the warps idle.
 static int64_t plan_chunk(int64_t numel) {
-    int64_t c = 2048;
+    int64_t c = 1024;
     while (c > 256 && numel / c < 64 * 148) c /= 2;
     return c;
 }
@@ -1174,11 +1201,11 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     uint8_t *host = static_cast<uint8_t *>(std::calloc(1, need));
     if (!host) return fail(QLORA_ERR_ARG, "no host memory for the plan (%zu bytes)", need);
     optim::Chunk *c = reinterpret_cast<optim::Chunk *>(host + sizeof(optim::PlanHead));
-    int32_t grad_only = 0;
+    int32_t kinds = 0;
     for (int64_t i = 0; i < count; ++i) {
         const qlora_adamw_tensor &t = tensors[i];
         const bool only = (t.flags & QLORA_OPT_GRAD_ONLY) != 0, eight = (t.flags & QLORA_OPT_STATE_8BIT) != 0;
-        if (only && t.numel) grad_only = 1;
+        if (t.numel) kinds |= only ? kPlanGradOnly : eight ? optim::kKind8 : optim::kKind32;
         const int64_t pb = (t.flags & QLORA_OPT_PARAM_BF16) ? 2 : 4, gb = (t.flags & QLORA_OPT_GRAD_BF16) ? 2 : 4, sb = eight ? 1 : 4;
         auto at = [](const void *base, int64_t off) { return base ? uint64_t(reinterpret_cast<uintptr_t>(base)) + uint64_t(off) : 0; };
         for (int64_t e = 0; e < t.numel; e += chunk, ++c) {
@@ -1204,7 +1231,7 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     plan->chunks = nchunks;
     plan->tensors = count;
     plan->numel = numel;
-    plan->grad_only = grad_only;
+    plan->kinds = kinds;
     plan->magic = kPlanMagic;
     return QLORA_OK;
 }
@@ -1219,16 +1246,16 @@ static const optim::Chunk *plan_list(const qlora_adamw_plan *plan) {
     return reinterpret_cast<const optim::Chunk *>(plan_head(plan) + 1);
 }
 // CTAs of a pass over the plan's chunks: enough warps for every chunk, at most `per_sm` CTAs per SM
-static unsigned plan_grid(const qlora_adamw_plan *plan, int per_sm) {
-    return static_cast<unsigned>(std::max<int64_t>(
-        1, std::min<int64_t>({ceil_div(plan->chunks, optim::kWarps), int64_t(per_sm) * sm_count(), optim::kPartials})));
+static dim3 plan_grid(const qlora_adamw_plan *plan, int per_sm) {
+    return dim3(static_cast<unsigned>(std::max<int64_t>(
+        1, std::min<int64_t>({ceil_div(plan->chunks, optim::kWarps), int64_t(per_sm) * sm_count(), optim::kPartials}))));
 }
 
 qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double beta1, double beta2, double eps,
                               int64_t step, const float *grad_scale, const float *lr_dev, int64_t *step_dev,
                               void *stream) {
     QL_TRY(check_plan(plan));
-    if (plan->grad_only) return fail(QLORA_ERR_ARG, "the plan holds QLORA_OPT_GRAD_ONLY tensors");
+    if (plan->kinds & kPlanGradOnly) return fail(QLORA_ERR_ARG, "the plan holds QLORA_OPT_GRAD_ONLY tensors");
     if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1)) return fail(QLORA_ERR_ARG, "betas must be in [0, 1)");
     if (!(eps >= 0) || !std::isfinite(eps)) return fail(QLORA_ERR_ARG, "eps must be finite and not negative");
     if (!lr_dev && !(lr >= 0 && std::isfinite(lr))) return fail(QLORA_ERR_ARG, "lr must be finite and not negative");
@@ -1245,19 +1272,29 @@ qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double be
     a.step_dev = step_dev;
     a.beta1 = beta1;
     a.beta2 = beta2;
+    a.eps = eps;
     a.nchunks = plan->chunks;
     a.lr = lr_dev ? 0.f : static_cast<float>(lr);
     a.b1 = static_cast<float>(beta1);
     a.w1 = static_cast<float>(1.0 - beta1);
     a.b2 = static_cast<float>(beta2);
     a.w2 = static_cast<float>(1.0 - beta2);
-    a.eps = static_cast<float>(eps);
     if (!step_dev) {
-        a.ibc1 = static_cast<float>(1.0 / (1.0 - std::pow(beta1, double(step))));
-        a.ibc2 = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, double(step))));
+        const double bc1 = 1.0 - std::pow(beta1, double(step));
+        a.ds = static_cast<float>(bc1 / std::sqrt(1.0 - std::pow(beta2, double(step))));
+        a.de = static_cast<float>(bc1 * eps);
     }
-    optim::adamw_kernel<<<plan_grid(plan, 8), optim::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
-    return launch_check("adamw_kernel launch");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const char *what = "adamw_kernel launch";
+    switch (plan->kinds) {
+        case optim::kKind32:
+            return launch_pdl(what, optim::adamw_kernel<optim::kKind32>, plan_grid(plan, optim::kCtas32), optim::kThreads, 0, st, a);
+        case optim::kKind8:
+            return launch_pdl(what, optim::adamw_kernel<optim::kKind8>, plan_grid(plan, optim::kCtas8), optim::kThreads, 0, st, a);
+        default:
+            return launch_pdl(what, optim::adamw_kernel<optim::kKind32 | optim::kKind8>, plan_grid(plan, optim::kCtas8),
+                              optim::kThreads, 0, st, a);
+    }
 }
 
 qlora_status qlora_grad_norm(const qlora_adamw_plan *plan, float max_norm, float *out, void *stream) {
@@ -1266,9 +1303,8 @@ qlora_status qlora_grad_norm(const qlora_adamw_plan *plan, float max_norm, float
     if (!out) return fail(QLORA_ERR_ARG, "out is NULL");
     if (reinterpret_cast<uintptr_t>(out) & 3) return fail(QLORA_ERR_ALIGN, "out must be 4-byte aligned");
     QL_TRY(require_sm100());
-    optim::grad_norm_kernel<<<plan_grid(plan, 8), optim::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-        plan_list(plan), plan_head(plan), plan->chunks, max_norm, out);
-    return launch_check("grad_norm_kernel launch");
+    return launch_pdl("grad_norm_kernel launch", optim::grad_norm_kernel, plan_grid(plan, 8), optim::kThreads, 0,
+                      static_cast<cudaStream_t>(stream), plan_list(plan), plan_head(plan), plan->chunks, max_norm, out);
 }
 
 static qlora_status check_adam8(const void *codes, int kind, const float *steps, const float *x, int64_t numel) {
@@ -1280,8 +1316,8 @@ static qlora_status check_adam8(const void *codes, int kind, const float *steps,
     if (reinterpret_cast<uintptr_t>(steps) & 3) return fail(QLORA_ERR_ALIGN, "steps must be 4-byte aligned");
     return QLORA_OK;
 }
-static unsigned adam8_grid(int64_t numel) {
-    return static_cast<unsigned>(std::min<int64_t>(ceil_div(numel, optim::kBlock * optim::kWarps), int64_t(sm_count()) * 32));
+static dim3 adam8_grid(int64_t numel) {
+    return dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(numel, optim::kBlock * optim::kWarps), int64_t(sm_count()) * 32)));
 }
 
 qlora_status qlora_adam8_encode(const float *x, int kind, void *codes, float *steps, int64_t numel, void *stream) {
@@ -1290,9 +1326,9 @@ qlora_status qlora_adam8_encode(const float *x, int kind, void *codes, float *st
     QL_TRY(require_sm100());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t *c = static_cast<uint8_t *>(codes);
-    if (kind == QLORA_ADAM8_SECOND) optim::adam8_encode_kernel<true><<<adam8_grid(numel), optim::kThreads, 0, st>>>(x, c, steps, numel);
-    else optim::adam8_encode_kernel<false><<<adam8_grid(numel), optim::kThreads, 0, st>>>(x, c, steps, numel);
-    return launch_check("adam8_encode_kernel launch");
+    return launch_pdl("adam8_encode_kernel launch",
+                      kind == QLORA_ADAM8_SECOND ? optim::adam8_encode_kernel<true> : optim::adam8_encode_kernel<false>,
+                      adam8_grid(numel), optim::kThreads, 0, st, x, c, steps, numel);
 }
 
 qlora_status qlora_adam8_decode(const void *codes, int kind, const float *steps, float *x, int64_t numel, void *stream) {
@@ -1301,9 +1337,9 @@ qlora_status qlora_adam8_decode(const void *codes, int kind, const float *steps,
     QL_TRY(require_sm100());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const uint8_t *c = static_cast<const uint8_t *>(codes);
-    if (kind == QLORA_ADAM8_SECOND) optim::adam8_decode_kernel<true><<<adam8_grid(numel), optim::kThreads, 0, st>>>(c, steps, x, numel);
-    else optim::adam8_decode_kernel<false><<<adam8_grid(numel), optim::kThreads, 0, st>>>(c, steps, x, numel);
-    return launch_check("adam8_decode_kernel launch");
+    return launch_pdl("adam8_decode_kernel launch",
+                      kind == QLORA_ADAM8_SECOND ? optim::adam8_decode_kernel<true> : optim::adam8_decode_kernel<false>,
+                      adam8_grid(numel), optim::kThreads, 0, st, c, steps, x, numel);
 }
 
 }  // extern "C"

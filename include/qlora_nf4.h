@@ -368,7 +368,7 @@ typedef struct {
 typedef struct {
     void *buffer;
     int64_t chunks, tensors, numel;
-    int32_t grad_only, magic;
+    int32_t kinds, magic;
     int64_t reserved;
 } qlora_adamw_plan;
 

@@ -2,9 +2,9 @@
 
 Moments, codes and block steps must match bit for bit (every rounding up to the code is
 fixed).  A parameter p' = p - lr (decay p + u) must lie within the roundings of its last
-operations: u = fdividef(m ibc1, w ibc2 + eps) takes 1 + 1 half-ulps for ibc1 and its product,
-1 each for the root w, ibc2, the fused add, and 4 for the quotient (2 ulp), the inner fused
-add 1, lr * lr_scale 2: at most 12, bounded here by 16 of 2^-24 relative to lr (|decay p| + |u|);
+operations: u = m / (w ds + de) takes 2 of 2^-24 for the approximate root w, 1 each for ds, de and
+the fused add, 2 for the approximate reciprocal, 1 for the product, the inner fused add 1,
+lr * lr_scale 2: at most 11, bounded here by 16 of 2^-24 relative to lr (|decay p| + |u|);
 the outer fused add and, for bf16, the last rounding take half a step of p' each."""
 import numpy as np
 import pytest
@@ -110,6 +110,7 @@ def test_adam8_codes_at_every_border(top, dtype):
 def test_adam8_round_trip_matches_oracle(n):
     g = torch.Generator().manual_seed(n)
     x = _rand(g, n, 3.0)
+    x[n // 2] = -0.0
     for dtype, top in ((torch.int8, 127), (torch.uint8, 255)):
         src = x if top == 127 else x * x
         codes = torch.empty(n + 9, dtype=dtype, device=DEV).fill_(77)
@@ -245,6 +246,35 @@ def test_non_finite_gradients():
             assert torch.isnan(t.exp_avg_step).tolist() == [False, True, True]
             assert not t.exp_avg[256:].any() and not t.exp_avg_sq[256:].any()
         q.qlora_sync_status()
+
+
+@pytest.mark.parametrize("size", [1e-16, 3e-19, 1e-21])
+def test_tiny_gradients(size):
+    # second moments below 2^-126 and steps at the edge of the code's range; eps = 0 keeps the ratio m / sqrt(v)
+    g = torch.Generator().manual_seed(18)
+    n = 1500
+    for bits in (32, 8):
+        t = q.AdamWTensor.zeros(torch.zeros(n, device=DEV), (_rand(g, n) / 1e-3 * size).to(DEV), bits=bits)
+        plan, mo = q.qlora_adamw_plan_init([t]), Model(t)
+        for k in (1, 2):
+            q.qlora_adamw_step(plan, 1e-3, k, eps=0.0)
+            q.qlora_sync_status()
+            m, v, w = T.adamw_moments(_np(t.grad), None, mo.m, mo.v, B1, B2)
+            live = v > 0                                   # below that the square is zero and the formula has no value
+            want, u = T.adamw_param(mo.p[live], m[live], v[live], k, 1e-3, 0.0, B1, B2, 0.0)
+            got = _np(t.param)
+            assert (np.abs(got[live] - want) <= 16 * 2.0 ** -24 * 1e-3 * np.abs(u) + 2.0 ** -24 * np.abs(want)).all(), (bits, k)
+            if bits == 8:
+                for codes, steps, x, top in ((t.exp_avg, t.exp_avg_step, m, 127), (t.exp_avg_sq, t.exp_avg_sq_step, w, 255)):
+                    ck, d = T.adam8_encode(x, top)
+                    assert np.array_equal(codes.cpu().numpy().astype(np.int64), ck) and np.array_equal(_bits(steps.cpu()), _bits(d))
+                mo.m, w = T.adam8_decode(*T.adam8_encode(m, 127)), T.adam8_decode(*T.adam8_encode(w, 255))
+                mo.v = T.rn32(w * w)
+            else:
+                assert np.array_equal(_bits(t.exp_avg.cpu()), _bits(m)) and np.array_equal(_bits(t.exp_avg_sq.cpu()), _bits(v))
+                mo.m, mo.v = m, v
+            t.param.nan_to_num_(0.0, 0.0, 0.0)
+            mo.p = _np(t.param)
 
 
 def test_step_on_another_stream():
