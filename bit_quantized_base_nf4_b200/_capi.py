@@ -45,8 +45,8 @@ class AdamWTensorC(ctypes.Structure):
 
 
 class AdamWPlanC(ctypes.Structure):
-    _fields_ = [("buffer", ctypes.c_void_p), ("chunks", ctypes.c_int64), ("tensors", ctypes.c_int64),
-                ("numel", ctypes.c_int64), ("kinds", ctypes.c_int32), ("magic", ctypes.c_int32),
+    _fields_ = [("buffer", ctypes.c_void_p), ("chunks", ctypes.c_int64), ("chunks32", ctypes.c_int64),
+                ("numel", ctypes.c_int64), ("grad_only", ctypes.c_int32), ("magic", ctypes.c_int32),
                 ("reserved", ctypes.c_int64)]
 
 

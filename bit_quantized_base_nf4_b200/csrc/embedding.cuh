@@ -59,6 +59,13 @@ __device__ __forceinline__ void scale_words(const ScaleSrc &s, int64_t b64, uint
     }
 }
 
+// 32-bit words of 8 elements of a table
+template <int kTable>
+constexpr int kWordsOf = kTable == kTableNf4 ? 1 : kTable == kTableQ8 ? 2 : kTable == kTableBf16 ? 4 : 8;
+__device__ __forceinline__ float level_at(const float *levels, uint32_t byte_offset) {
+    return *reinterpret_cast<const float *>(reinterpret_cast<const char *>(levels) + byte_offset);
+}
+
 // A warp takes one segment of one token's row: its id, then every code and scale load of the
 // segment at once, 8 elements per lane and step, so that a bf16 output is one 16-byte store.
 // CTAs: x over tokens, y over groups of 2^seg_shift segments.
@@ -84,82 +91,85 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const FwdArgs a)
     if (!ok && lane == 0) report_bad_id();
     const int64_t row = ok ? id * a.H : 0;
 
-    uint4 raw[kUnroll], raw2[kTable == kTableF32 ? kUnroll : 1];
+    uint32_t raw[kUnroll][kWordsOf<kTable>];
     uint32_t sa[kUnroll];
     float sd[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         const int64_t e = e0 + u * 256;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        sa[u] = 0;
-        sd[u] = 0.f;
-        if (kTable == kTableF32) raw2[u] = make_uint4(0, 0, 0, 0);
-        if (e < a.H && ok) {
-            if (kTable == kTableNf4) {
-                raw[u].x = __ldcg(reinterpret_cast<const uint32_t *>(a.table) + ((row + e) >> 3));
-                scale_words(a.sc, (row + e) >> 6, sa[u], sd[u]);
-            } else if (kTable == kTableQ8) {
-                const uint2 q = __ldcg(reinterpret_cast<const uint2 *>(a.table) + ((row + e) >> 3));
-                raw[u].x = q.x;
-                raw[u].y = q.y;
-                sa[u] = __ldcg(a.d8 + ((row + e) >> 5));
-            } else if (kTable == kTableBf16) {
-                raw[u] = __ldcg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 3));
-            } else {
-                raw[u] = __ldcg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 2));
-                raw2[u] = __ldcg(reinterpret_cast<const uint4 *>(a.table) + ((row + e) >> 2) + 1);
+        if (e >= a.H || !ok) continue;
+        const int64_t at = row + e;
+        if (kTable == kTableNf4) {
+            raw[u][0] = __ldcg(reinterpret_cast<const uint32_t *>(a.table) + (at >> 3));
+            scale_words(a.sc, at >> 6, sa[u], sd[u]);
+        } else if (kTable == kTableQ8) {
+            const uint2 q = __ldcg(reinterpret_cast<const uint2 *>(a.table) + (at >> 3));
+            raw[u][0] = q.x;
+            raw[u][1 % kWordsOf<kTable>] = q.y;
+            sa[u] = __ldcg(a.d8 + (at >> 5));
+        } else {
+#pragma unroll
+            for (int h = 0; h < kWordsOf<kTable> / 4; ++h) {
+                const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const char *>(a.table) + at * (kTable == kTableBf16 ? 2 : 4)) + h);
+                raw[u][(4 * h) % kWordsOf<kTable>] = x.x, raw[u][(4 * h + 1) % kWordsOf<kTable>] = x.y;
+                raw[u][(4 * h + 2) % kWordsOf<kTable>] = x.z, raw[u][(4 * h + 3) % kWordsOf<kTable>] = x.w;
             }
         }
     }
+    const uint64_t scale = pack2(a.scale, a.scale);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
         const int64_t e = e0 + u * 256;
         if (e >= a.H) break;
-        float w[8];
-        if (kTable == kTableNf4) {
-            const float s = scale_of(a.sc, sa[u], sd[u]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(s_lv[(raw[u].x >> (4 * j)) & 15u], s);
-        } else if (kTable == kTableQ8) {
-            const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sa[u])));
-            const float magic = 8388736.f;   // 2^23 + 128
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t b = (j < 4 ? raw[u].x : raw[u].y) ^ 0x80808080u;
-                w[j] = __fmul_rn(__uint_as_float(__byte_perm(b, 0x4B000000u, 0x7650 + (j & 3))) - magic, s);
-            }
-        } else if (kTable == kTableBf16) {
-            const uint32_t x[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[2 * j] = __uint_as_float(x[j] << 16);
-                w[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
-            }
-        } else {
-            const uint32_t x[8] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w, raw2[u].x, raw2[u].y, raw2[u].z, raw2[u].w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(x[j]);
-        }
+        uint64_t w[4] = {0, 0, 0, 0};              // pairs of elements
         if (ok) {
+            if (kTable == kTableNf4) {
+                // byte offsets 4 c into the level table, four codes at a time; level(c) of two neighbours
+                const float f = scale_of(a.sc, sa[u], sd[u]);
+                const uint32_t lo = (raw[u][0] << 2) & 0x3C3C3C3Cu, hi = (raw[u][0] >> 2) & 0x3C3C3C3Cu;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(w[j], a.scale);
-        } else {
+                for (int j = 0; j < 4; ++j)
+                    w[j] = mul2(pack2(level_at(s_lv, __byte_perm(lo, 0u, 0x4440u + j)), level_at(s_lv, __byte_perm(hi, 0u, 0x4440u + j))),
+                                pack2(f, f));
+            } else if (kTable == kTableQ8) {
+                const float f = __half2float(__ushort_as_half(static_cast<unsigned short>(sa[u])));
+                const uint64_t magic = pack2(-8388736.f, -8388736.f);   // -(2^23 + 128)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 0.f;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t b = raw[u][(j / 2) % kWordsOf<kTable>] ^ 0x80808080u;
+                    w[j] = mul2(add2(pack2(__uint_as_float(__byte_perm(b, 0x4B000000u, 0x7650 + 2 * (j & 1))),
+                                           __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7651 + 2 * (j & 1)))), magic), pack2(f, f));
+                }
+            } else if (kTable == kTableBf16) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t x = raw[u][j % kWordsOf<kTable>];
+                    w[j] = pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = pack2(__uint_as_float(raw[u][(2 * j) % kWordsOf<kTable>]), __uint_as_float(raw[u][(2 * j + 1) % kWordsOf<kTable>]));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], scale);
         }
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) unpack2(w[j], y[2 * j], y[2 * j + 1]);
         const int64_t o = t * a.H + e;
         if (kOutBf16) {
             uint32_t b[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(w[2 * j], w[2 * j + 1]);
+                const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
                 b[j] = *reinterpret_cast<const uint32_t *>(&p);
             }
             reinterpret_cast<uint4 *>(a.out)[o >> 3] = make_uint4(b[0], b[1], b[2], b[3]);
         } else {
             float4 *dst = reinterpret_cast<float4 *>(a.out) + (o >> 2);
-            dst[0] = make_float4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_float4(w[4], w[5], w[6], w[7]);
+            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
         }
     }
 }
@@ -172,10 +182,9 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const FwdArgs a)
 //   join    adds the partial sums of each such id in order and writes its row;
 //   zero    (unless the gradient is added) zeroes the rows that no token names.
 // Every sum is float32, in an order fixed by the ids alone: results repeat bit for bit.
-// All four overlap: each starts once the one before it has (programmatic dependent launch).  `zero`
-// needs the ids only, not the sort, so the table's writes, nearly all of the time when the table is
-// large, run beside the sort and the reduction; it waits for the others at its end instead, so that
-// its completion means the whole call's.
+// The last three overlap: each starts once the one before it has started (programmatic dependent
+// launch).  `zero` needs the sort only, so its writes, nearly all of the time when the table is large, run
+// beside the reduction; its last CTA waits for the join, so that its completion means the whole call's.
 constexpr int kSortCtas = 8;            // one cluster sorts: bins and counts meet in shared memory
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -196,6 +205,8 @@ struct GradArgs {
     float scale;
     int chunk;                   // sorted tokens per chunk of the reduction
     int64_t nchunks;
+    uint32_t *named;             // bit v: a token names row v (when the gradient is written, not added)
+    int zero_rows;               // rows a CTA zeroes
     float *part;                 // [nchunks][2][H] partial sums: of the run at a chunk's first token, of its last run
 };
 
@@ -258,6 +269,7 @@ __device__ void sort_tokens(const GradArgs &a, uint32_t *smem) {
             for (int u = 0; u < kSortBatch; ++u) {
                 if (i + 32 * u >= i_hi) break;
                 const bool in = i + 32 * u + lane < i_hi;
+                if (pass == 0 && !a.accumulate && in && k[u] < a.V) atomicOr(a.named + (k[u] >> 5), 1u << (k[u] & 31));
                 const uint32_t d = in ? (k[u] >> shift) & (bins - 1) : uint32_t(kMaxBins);   // idle lanes match none
                 const uint32_t same = __match_any_sync(0xffffffffu, d);
                 if (in && (same & ((1u << lane) - 1u)) == 0) my[d] += __popc(same);
@@ -267,12 +279,13 @@ __device__ void sort_tokens(const GradArgs &a, uint32_t *smem) {
         __syncthreads();
         // per bin: counts of lower warps, and this CTA's total
         if (tid < bins) {
-            uint32_t sum = 0;
-#pragma unroll 8
+            uint32_t sum = 0, n[kSortWarps];
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) n[w] = hist[w * kMaxBins + tid];
+#pragma unroll
             for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t n = hist[w * kMaxBins + tid];
                 hist[w * kMaxBins + tid] = sum;
-                sum += n;
+                sum += n[w];
             }
             total[tid] = sum;
         }
@@ -333,42 +346,43 @@ __device__ void sort_tokens(const GradArgs &a, uint32_t *smem) {
 
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) embed_sort_kernel(const GradArgs a) {
     extern __shared__ uint32_t sort_smem[];
-    pdl_wait();                 // before the release: what starts after this kernel may rely on the inputs
     pdl_launch_dependents();
+    pdl_wait();
+    if (!a.accumulate) {        // which rows are named; the marks are set by the sort's first pass
+        for (int64_t i = int64_t(cluster_rank()) * kSortThreads + threadIdx.x; i < (a.V + 31) / 32; i += kSortCtas * kSortThreads)
+            __stcg(a.named + i, 0u);
+        cluster_barrier();
+    }
     sort_tokens(a, sort_smem);
 }
 
-// Zero: a CTA owns an equal run of rows, marks the named ones in a bitmap (kMaskRows rows at a time,
-// reading every id from L2 for itself, so that it need not wait for the sort) and zeroes the others.
-constexpr int kZeroThreads = 512;
-constexpr int kMaskRows = 32768;
-__global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(const GradArgs a, int first) {
-    __shared__ uint32_t mask[kMaskRows / 32];
+// Zero: a CTA of 256 threads for about 16 KB of rows, in the order of the table.  (A grid of two CTAs per SM
+// that strides over the rows wrote 6.0 TB/s, this order 7.2: what is written at any time lies close together.)
+constexpr int kZeroThreads = 256;
+__global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(const GradArgs a) {
     pdl_launch_dependents();
-    if (first) pdl_wait();      // no sort before this kernel: the inputs may still be on their way
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (a.T == 0) pdl_wait();   // otherwise the reduction has let this kernel start, after its own wait for the sort
     const int64_t row_words = a.H * (a.de_bf16 ? 2 : 4) / 16;
-    int64_t lo = a.V * blockIdx.x / gridDim.x;
-    const int64_t hi = a.V * (blockIdx.x + 1) / gridDim.x;
-    for (; lo < hi; lo += kMaskRows) {
-        const int64_t end = min(lo + int64_t(kMaskRows), hi);
-        __syncthreads();
-        for (int i = tid; i < (end - lo + 31) / 32; i += kZeroThreads) mask[i] = 0;
-        __syncthreads();
-#pragma unroll 8
-        for (int64_t t = tid; t < a.T; t += kZeroThreads) {
-            const int64_t id = id_at(a.ids, t);
-            if (id >= lo && id < end && id != a.pad) atomicOr(mask + ((id - lo) >> 5), 1u << ((id - lo) & 31));
-        }
-        __syncthreads();
-        for (int64_t r = lo + warp; r < end; r += kZeroThreads / 32) {
-            if ((mask[(r - lo) >> 5] >> ((r - lo) & 31)) & 1u) continue;
+    const int64_t end = min((blockIdx.x + int64_t(1)) * a.zero_rows, a.V);
+    if (row_words >= kZeroThreads) {
+        for (int64_t r = blockIdx.x * int64_t(a.zero_rows); r < end; ++r) {
+            if (a.T > 0 && ((__ldcg(a.named + (r >> 5)) >> (r & 31)) & 1u)) continue;
             uint4 *dst = static_cast<uint4 *>(a.dE) + r * row_words;
 #pragma unroll 4
-            for (int64_t i = lane; i < row_words; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+            for (int64_t i = threadIdx.x; i < row_words; i += kZeroThreads) dst[i] = make_uint4(0, 0, 0, 0);
+        }
+    } else {
+        // short rows: the CTA's words as one run (at most 1024 + 255 rows' words, 32-bit)
+        const int64_t r0 = blockIdx.x * int64_t(a.zero_rows);
+        const uint32_t words = static_cast<uint32_t>((end - r0) * row_words), rw = static_cast<uint32_t>(row_words);
+        uint4 *dst = static_cast<uint4 *>(a.dE) + r0 * row_words;
+        for (uint32_t i = threadIdx.x; i < words; i += kZeroThreads) {
+            const int64_t r = r0 + i / rw;
+            if (a.T > 0 && ((__ldcg(a.named + (r >> 5)) >> (r & 31)) & 1u)) continue;
+            dst[i] = make_uint4(0, 0, 0, 0);
         }
     }
-    if (!first) pdl_wait();
+    if (blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // kN (4 or 8) elements of a row of dY or dE as loaded, and as floats
@@ -429,8 +443,8 @@ constexpr int kBatch = 4;
 template <bool kDyBf16, bool kDeBf16, bool kAdd>
 __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArgs a) {
     __shared__ uint32_t s_id[kMaxChunk + 2], s_pos[kMaxChunk];   // s_id[0]: the token before the chunk; last + 1: after it
+    pdl_wait();                 // before the release: `zero` may rely on the sort
     pdl_launch_dependents();
-    pdl_wait();
     const uint32_t *ids = a.key[a.passes & 1], *pos = a.pos[a.passes & 1];
     const int64_t ch = blockIdx.x;
     const int64_t i0 = ch * a.chunk;
@@ -484,10 +498,10 @@ __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArg
 
 // Join: an id whose tokens cross a chunk border belongs to the chunk where it starts; its row is that
 // chunk's partial sum and those of the next chunks' first runs, as far as they have the same id.  A warp
-// takes one chunk and 128 columns; an id with more than kLongJoin partial sums is added by all eight warps,
+// takes one chunk and 512 columns; an id with more than kLongJoin partial sums is added by all eight warps,
 // each over an equal part of the list, and the eight sums in order.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinCols = 128;
+constexpr int kJoinCols = 512;         // four runs of 128
 constexpr int kLongJoin = 32;
 __device__ __forceinline__ void add4(float4 &s, const float4 x) {
     s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
@@ -545,12 +559,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradA
             end = end_of_id(a, ids, id, ch + 1, lane);
         }
     }
-    Raw<kDeBf16, 4> old;
-    old.zero();
-    if (end && end - ch <= kLongJoin && c < a.H) {
-        if (a.accumulate) old.load(a.dE, int64_t(id) * a.H + c);
-        const float4 s = sum_firsts(a, load_part(a, 2 * ch + slot, c), ch + 1, end, c);
-        write_row<kDeBf16, 4>(a, id, c, reinterpret_cast<const float *>(&s), old);
+    if (end && end - ch <= kLongJoin) {
+#pragma unroll
+        for (int q = 0; q < kJoinCols / 128; ++q) {
+            const int64_t cq = c + 128 * q;
+            if (cq >= a.H) break;
+            Raw<kDeBf16, 4> old;
+            old.zero();
+            if (a.accumulate) old.load(a.dE, int64_t(id) * a.H + cq);
+            const float4 s = sum_firsts(a, load_part(a, 2 * ch + slot, cq), ch + 1, end, cq);
+            write_row<kDeBf16, 4>(a, id, cq, reinterpret_cast<const float *>(&s), old);
+        }
     }
     if (lane == 0) {
         s_end[warp] = end && end - ch > kLongJoin ? end : 0;
@@ -561,20 +580,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradA
     for (int w = 0; w < kJoinWarps; ++w) {
         if (!s_end[w]) continue;                                  // the same for the whole block
         const int64_t lo = ch - warp + w + 1, n = s_end[w] - lo;  // first-run partials of chunks [lo, lo + n)
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < a.H) {
-            if (warp == 0) s = load_part(a, 2 * (lo - 1) + s_slot[w], c);
-            if (warp == 0 && a.accumulate) old.load(a.dE, int64_t(s_id[w]) * a.H + c);
-            s = sum_firsts(a, s, lo + n * warp / kJoinWarps, lo + n * (warp + 1) / kJoinWarps, c);
-        }
-        s_part[warp][lane] = s;
-        __syncthreads();
-        if (warp == 0 && c < a.H) {
+        for (int64_t cq = c; cq < c - lane * 4 + kJoinCols && cq - lane * 4 < a.H; cq += 128) {
+            Raw<kDeBf16, 4> old;
+            old.zero();
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (cq < a.H) {
+                if (warp == 0) s = load_part(a, 2 * (lo - 1) + s_slot[w], cq);
+                if (warp == 0 && a.accumulate) old.load(a.dE, int64_t(s_id[w]) * a.H + cq);
+                s = sum_firsts(a, s, lo + n * warp / kJoinWarps, lo + n * (warp + 1) / kJoinWarps, cq);
+            }
+            s_part[warp][lane] = s;
+            __syncthreads();
+            if (warp == 0 && cq < a.H) {
 #pragma unroll
-            for (int i = 1; i < kJoinWarps; ++i) add4(s, s_part[i][lane]);
-            write_row<kDeBf16, 4>(a, s_id[w], c, reinterpret_cast<const float *>(&s), old);
+                for (int i = 1; i < kJoinWarps; ++i) add4(s, s_part[i][lane]);
+                write_row<kDeBf16, 4>(a, s_id[w], cq, reinterpret_cast<const float *>(&s), old);
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 

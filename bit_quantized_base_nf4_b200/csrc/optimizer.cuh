@@ -29,7 +29,7 @@ namespace optim {
 constexpr int kBlock = 256;          // values per 8-bit block: one warp step, 8 per lane
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPartials = 2048;      // slots for per-CTA partial sums of the norm
+constexpr int kPartials = 4096;      // most CTAs of the norm: slots for their partial sums
 constexpr int kTopM = 127, kTopW = 255;
 
 enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4 };
@@ -46,11 +46,12 @@ struct alignas(16) Chunk {
 };
 static_assert(sizeof(Chunk) == 80, "a chunk is 20 words");
 
-// Head of the plan buffer: the CTA ticket of the norm and of the device step counter, then the
-// partial sums.  Every kernel leaves the ticket at zero.
+// Head of the plan buffer: the CTA ticket of the norm (left at zero), the scalars of a step counted on
+// the device, and the norm's partial sums.
 struct alignas(256) PlanHead {
     unsigned int ticket;
-    unsigned int unused[63];
+    float ds, de;
+    unsigned int unused[61];
     double partial[kPartials];
 };
 
@@ -149,23 +150,32 @@ __device__ __forceinline__ void store_codes(uint64_t base, int64_t i0, int rem, 
     }
 }
 
-// k of byte j as a float: the byte becomes the low mantissa byte of 2^23 (one permute and one
-// exact subtraction; no integer conversion, whose pipe is eight times narrower)
+// Bytes j and j + 1 of w as floats k: a byte becomes the low mantissa byte of 2^23 (one permute each and
+// one exact subtraction; no integer conversion, whose pipe is eight times narrower)
 template <bool kSigned>
-__device__ __forceinline__ float code_value(uint32_t w, int j) {
+__device__ __forceinline__ uint64_t code_pair(uint32_t w, int j) {
     const uint32_t u = kSigned ? w ^ 0x80808080u : w;
-    const float magic = kSigned ? 8388736.f : 8388608.f;   // 2^23 (+ 128)
-    return __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7650 + j)) - magic;
+    const float magic = kSigned ? -8388736.f : -8388608.f;   // -(2^23 (+ 128))
+    return add2(pack2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7650 + j)),
+                      __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7651 + j))), pack2(magic, magic));
 }
-// x[0..7] = k |k| d of a lane's codes
-template <bool kSigned>
-__device__ __forceinline__ void decode8(const uint32_t *c, float d, float *x) {
+// A lane's 8 values as 4 pairs: k |k| d, or the square of k^2 d
+template <bool kSecond>
+__device__ __forceinline__ void decode8(const uint32_t *c, float d, uint64_t *x) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float k = code_value<kSigned>(c[i >> 2], i & 3);
-        x[i] = __fmul_rn(__fmul_rn(k, fabsf(k)), d);
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t k = code_pair<!kSecond>(c[i >> 1], 2 * (i & 1));
+        if (kSecond) {
+            const uint64_t w = mul2(mul2(k, k), pack2(d, d));
+            x[i] = mul2(w, w);
+        } else {
+            float a, b;
+            unpack2(k, a, b);
+            x[i] = mul2(pack2(__fmul_rn(a, fabsf(a)), __fmul_rn(b, fabsf(b))), pack2(d, d));
+        }
     }
 }
+
 // roots to 2^-23: kFtz takes inputs below 2^-126 as 0
 template <bool kFtz>
 __device__ __forceinline__ float sqrt_approx(float x) {
@@ -179,62 +189,86 @@ __device__ __forceinline__ float rcp_approx(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// the larger magnitude as bits: an infinity is above every finite value, a NaN above that
-__device__ __forceinline__ uint32_t max_bits(uint32_t a, float x) { return max(a, __float_as_uint(x) & 0x7FFFFFFFu); }
-
-// A block's step d = RN(a / top^2) from the bits of its largest magnitude a, and RN(1 / d)
-__device__ __forceinline__ void block_step(uint32_t a_bits, float top2, float &d, float &inv) {
-    d = __fdiv_rn(__uint_as_float(a_bits), top2);
-    inv = __frcp_rn(d);
-    if (d < 1.17549435e-38f) d = 0.f, inv = 0.f;
-    if (a_bits >= 0x7F800000u) d = __uint_as_float(0x7FC00000u), inv = 0.f;
+// the larger of a and |x|; a NaN once seen stays
+__device__ __forceinline__ float max_nan(float a, float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(x)));
+    return r;
 }
 
-// Codes of a lane's 8 values given inv = RN(1 / d).  kSigned: x holds m.  Otherwise x holds v, of
+// A block's step d = RN(a / top^2) from its largest magnitude a, and RN(1 / d)
+__device__ __forceinline__ void block_step(float a, float top2, float &d, float &inv) {
+    d = __fdiv_rn(a, top2);
+    inv = __frcp_rn(d);
+    if (d < 1.17549435e-38f) d = 0.f, inv = 0.f;
+    if (!(a < INFINITY)) d = __uint_as_float(0x7FC00000u), inv = 0.f;
+}
+
+// Codes of a lane's 8 values given inv = RN(1 / d).  kSecond = false: x holds m.  Otherwise x holds v, of
 // which y = RN(RN(sqrt(v)) inv) is coded, and w its approximate root.  The candidate is the
-// nearest integer to an approximate sqrt(y - 1/4), good to 1e-4 for k up to 255 (relative errors of
-// 2^-22 each in root and product); only where that root lies within 2e-4 of a half is y formed
+// nearest integer to an approximate sqrt(y - 1/4): relative errors of 2^-23 for w and for the root and 2^-24 for
+// the product put it within 255 * 1.75 * 2^-23 = 5.4e-5.  Only where that root lies within 1e-4 of a half is y formed
 // exactly and the candidate checked against the borders.
 constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer in the low mantissa bits
-template <bool kSigned>
-__device__ __forceinline__ void encode8(const float *x, const float *w, float inv, uint32_t *c) {
-    float t[8], off = 0.f;
+template <bool kSecond>
+__device__ __forceinline__ void encode8(const float *x, const float *w, float inv, bool exact, uint32_t *c) {
+    uint32_t t[8];
+    float off = exact ? 1.f : 0.f;
+    const uint64_t magic = pack2(kMagic, kMagic), minus = pack2(-1.f, -1.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float r = sqrt_approx<true>(fmaxf(fmaf(kSigned ? fabsf(x[i]) : w[i], inv, -0.25f), 0.f));
-        t[i] = __fadd_rn(r, kMagic);
-        off = fmaxf(off, fabsf(r - __fsub_rn(t[i], kMagic)));
+    for (int i = 0; i < 8; i += 2) {
+        float z0, z1;
+        if (kSecond) {
+            unpack2(fma2(pack2(w[i], w[i + 1]), pack2(inv, inv), pack2(-0.25f, -0.25f)), z0, z1);
+        } else {
+            z0 = fmaf(fabsf(x[i]), inv, -0.25f);
+            z1 = fmaf(fabsf(x[i + 1]), inv, -0.25f);
+        }
+        z0 = sqrt_approx<true>(fmaxf(z0, 0.f));
+        z1 = sqrt_approx<true>(fmaxf(z1, 0.f));
+        if (!kSecond) {
+            z0 = copysignf(z0, x[i]);
+            z1 = copysignf(z1, x[i + 1]);
+        }
+        const uint64_t z = pack2(z0, z1), r = add2(z, magic);
+        float e0, e1, r0, r1;
+        unpack2(add2(z, fma2(r, minus, magic)), e0, e1);    // z - (r - magic)
+        off = fmaxf(off, fmaxf(fabsf(e0), fabsf(e1)));
+        unpack2(r, r0, r1);
+        t[i] = __float_as_uint(r0);
+        t[i + 1] = __float_as_uint(r1);
     }
-    if (off > 0.4998f) {
-#pragma unroll
+    if (off > 0.4999f) {
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-            const float y = __fmul_rn(kSigned ? fabsf(x[i]) : __fsqrt_rn(x[i]), inv), k = __fsub_rn(t[i], kMagic);
+            // places of x, w and t are picked without dynamic indexing
+            float xi = x[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) xi = i == j ? x[j] : xi;
+            const float y = __fmul_rn(kSecond ? __fsqrt_rn(xi) : fabsf(xi), inv);
+            float k = rintf(sqrt_approx<true>(fmaxf(__fsub_rn(y, 0.25f), 0.f)));
             // k^2 + k + 1/2 is exact: at most 17 significant bits
-            if (y > __fmaf_rn(k, k, k) + 0.5f) t[i] += 1.f;
-            else if (k > 0.f && y <= __fmaf_rn(k, k, -k) + 0.5f) t[i] -= 1.f;
+            if (y > __fmaf_rn(k, k, k) + 0.5f) k += 1.f;
+            else if (k > 0.f && y <= __fmaf_rn(k, k, -k) + 0.5f) k -= 1.f;
+            const uint32_t b = __float_as_uint(__fadd_rn(kSecond ? k : copysignf(k, xi), kMagic));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) t[j] = i == j ? b : t[j];
         }
     }
-    if (kSigned) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = __fadd_rn(copysignf(__fsub_rn(t[i], kMagic), x[i]), kMagic);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = __byte_perm(__float_as_uint(t[4 * h]), __float_as_uint(t[4 * h + 1]), 0x0040);
-        const uint32_t hi = __byte_perm(__float_as_uint(t[4 * h + 2]), __float_as_uint(t[4 * h + 3]), 0x0040);
-        c[h] = __byte_perm(lo, hi, 0x5410);
-    }
+    for (int h = 0; h < 2; ++h)
+        c[h] = __byte_perm(__byte_perm(t[4 * h], t[4 * h + 1], 0x0040), __byte_perm(t[4 * h + 2], t[4 * h + 3], 0x0040), 0x5410);
 }
 
 struct StepArgs {
     const Chunk *chunks;
-    PlanHead *head;
+    const PlanHead *head;
     const float *coef;         // clip coefficient on the device, or NULL
     const float *lr_dev;       // learning rate on the device, or NULL
-    int64_t *step_dev;         // number of steps taken, or NULL
-    double beta1, beta2, eps;
+    int counted;               // 1: ds and de are in the head (step_scalars_kernel)
     int64_t nchunks;
     float lr, b1, w1, b2, w2;  // w = 1 - b
+    float one;                 // 1, as a value that the compiler does not know
     float ds, de;              // (1 - b1^t) / sqrt(1 - b2^t) and (1 - b1^t) eps
 };
 
@@ -245,185 +279,384 @@ __device__ __forceinline__ double pow_int(double b, int64_t t) {
         if (t & 1) r *= b;
     return r;
 }
-
-// A chunk's addresses and settings, the same in every lane.
-struct View {
-    uint64_t p, copy, g, m, v, dm, dv;
-    int n;
-    uint32_t flags;
-    float lr, decay;
-};
-__device__ __forceinline__ View view_of(uint32_t word, float lr) {
-    View c;
-    c.p = word64(word, 0), c.copy = word64(word, 2), c.g = word64(word, 4), c.m = word64(word, 6);
-    c.v = word64(word, 8), c.dm = word64(word, 10), c.dv = word64(word, 12);
-    c.n = static_cast<int>(word32(word, 14));
-    c.flags = word32(word, 15);
-    c.lr = lr * __uint_as_float(word32(word, 16));
-    c.decay = __uint_as_float(word32(word, 17));
-    return c;
+// The scalars of a step whose number is kept on the device, and the count of it (one thread): a launch of
+// its own, because worked out by every CTA it cost each of them about 0.5 us of double-precision latency.
+__global__ void step_scalars_kernel(PlanHead *head, int64_t *step_dev, const float *coef, double beta1, double beta2, double eps) {
+    pdl_launch_dependents();
+    pdl_wait();
+    if (coef && !isfinite(__ldcg(coef))) return;
+    const int64_t t = *step_dev + 1;
+    *step_dev = t;
+    const double bc1 = 1.0 - pow_int(beta1, t);
+    head->ds = static_cast<float>(bc1 / sqrt(1.0 - pow_int(beta2, t)));
+    head->de = static_cast<float>(bc1 * eps);
 }
-// The step's scalars: denominators are (sqrt(v) ibc2 + eps) bc1 = sqrt(v) ds + de.
+
+// The step's scalars: denominators are (sqrt(v) ibc2 + eps) bc1 = sqrt(v) ds + de.  flush: the root may take
+// a v below 2^-126 as zero (its root, at most 1.1e-19, is then under 2^-24 of the denominator).
 struct Scalars {
-    float coef, ds, de;
+    float coef, lr, ds, de;
+    bool flush;
+};
+// false: the gradients held an infinity or a NaN, and nothing changes
+__device__ __forceinline__ bool read_scalars(const StepArgs &a, Scalars &s) {
+    s.coef = a.coef ? __ldcg(a.coef) : 1.f;          // a product with 1 changes nothing
+    s.lr = a.lr_dev ? __ldcg(a.lr_dev) : a.lr;
+    s.ds = a.counted ? __ldcg(&a.head->ds) : a.ds;
+    s.de = a.counted ? __ldcg(&a.head->de) : a.de;
+    s.flush = s.de >= 2e-12f * s.ds;
+    return isfinite(s.coef);
+}
+
+// A lane's 8 elements of a block of a parameter or gradient as loaded: what is not used yet takes no
+// conversion, so that a block's loads are all issued before the first of them is waited for.
+template <bool kBf16>
+struct Raw8 {
+    uint32_t w[kBf16 ? 4 : 8];
+    template <bool kFull>
+    __device__ __forceinline__ void load(uint64_t base, int64_t i0, int rem, int lane) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int e = h * 128 + lane * 4;
+            if (kFull && kBf16) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(base + 2 * (i0 + e));
+                w[2 * h] = x.x, w[2 * h + 1] = x.y;
+            } else if (kFull) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(base + 4 * (i0 + e));
+                w[4 * h] = x.x, w[4 * h + 1] = x.y, w[(4 * h + 2) % (kBf16 ? 4 : 8)] = x.z, w[(4 * h + 3) % (kBf16 ? 4 : 8)] = x.w;
+            } else {
+                uint32_t x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[j] = 0;
+                    if (e + j < rem)
+                        x[j] = kBf16 ? uint32_t(reinterpret_cast<const uint16_t *>(base)[i0 + e + j])
+                                     : reinterpret_cast<const uint32_t *>(base)[i0 + e + j];
+                }
+                if (kBf16) {
+                    w[2 * h] = x[0] | (x[1] << 16), w[2 * h + 1] = x[2] | (x[3] << 16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[(4 * h + j) % (kBf16 ? 4 : 8)] = x[j];
+                }
+            }
+        }
+    }
+    // elements 2 i and 2 i + 1
+    __device__ __forceinline__ uint64_t pair(int i) const {
+        if (kBf16) return pack2(__uint_as_float(w[i % 4] << 16), __uint_as_float(w[i % 4] & 0xFFFF0000u));
+        return pack2(__uint_as_float(w[(2 * i) % (kBf16 ? 4 : 8)]), __uint_as_float(w[(2 * i + 1) % (kBf16 ? 4 : 8)]));
+    }
 };
 
-// One block of 256 (kFull) or the rem < 256 last elements of a tensor.
-template <bool kState8, bool kPBf16, bool kGBf16, bool kFull>
-__device__ __forceinline__ void step_block(const StepArgs &a, const View &c, const Scalars &s, int64_t i0, int rem, int lane) {
-    float g[8], p[8], m[8], v[8], w[8];
-    uint32_t cm[2], cv[2];
-    float dm = 0.f, dv = 0.f;
-    if (kState8) {
-        load_codes<kFull>(c.m, i0, rem, lane, cm);
-        load_codes<kFull>(c.v, i0, rem, lane, cv);
-        dm = reinterpret_cast<const float *>(c.dm)[i0 / kBlock];
-        dv = reinterpret_cast<const float *>(c.dv)[i0 / kBlock];
-    } else {
-        load8<kFull>(c.m, false, i0, rem, lane, m);
-        load8<kFull>(c.v, false, i0, rem, lane, v);
-    }
-    load8<kFull>(c.g, kGBf16, i0, rem, lane, g);
-    load8<kFull>(c.p, kPBf16, i0, rem, lane, p);
-    if (kState8) {
-        decode8<true>(cm, dm, m);
-        decode8<false>(cv, dv, v);
+// The moments of pair i and the parameters, from g and the old moments.  Products and sums of the moments are
+// rounded one by one: the sum is a product with the argument `one`, because a plain paired product and
+// sum were merged into one rounding by the assembler (codes then differed).
+__device__ __forceinline__ void moments(const StepArgs &a, const Scalars &s, uint64_t g, uint64_t &m, uint64_t &v) {
+    const uint64_t one = pack2(a.one, a.one);
+    g = mul2(g, pack2(s.coef, s.coef));
+    m = fma2(mul2(pack2(a.b1, a.b1), m), one, mul2(pack2(a.w1, a.w1), g));
+    v = fma2(mul2(pack2(a.b2, a.b2), v), one, mul2(pack2(a.w2, a.w2), mul2(g, g)));
+}
+// the approximate roots w of a lane's 8 second moments
+__device__ __forceinline__ void roots(const Scalars &s, const float *v, float *w) {
+    if (s.flush) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], v[i]);
-    }
-    uint32_t am = 0, av = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float gi = __fmul_rn(g[i], s.coef);
-        m[i] = __fadd_rn(__fmul_rn(a.b1, m[i]), __fmul_rn(a.w1, gi));
-        v[i] = __fadd_rn(__fmul_rn(a.b2, v[i]), __fmul_rn(a.w2, __fmul_rn(gi, gi)));
-        w[i] = sqrt_approx<false>(v[i]);
-        p[i] = fmaf(-c.lr, fmaf(c.decay, p[i], m[i] * rcp_approx(fmaf(w[i], s.ds, s.de))), p[i]);
-        if (kState8 && (kFull || (i >> 2) * 128 + lane * 4 + (i & 3) < rem)) {
-            am = max_bits(am, m[i]);
-            av = max_bits(av, v[i]);
-        }
-    }
-    store8<kFull>(c.p, kPBf16, i0, rem, lane, p);
-    if (!kPBf16 && c.copy) store8<kFull>(c.copy, true, i0, rem, lane, p);
-    if (kState8) {
-        am = __reduce_max_sync(0xffffffffu, am);
-        av = __reduce_max_sync(0xffffffffu, av);
-        // the root is monotonic, so the largest root is the root of the largest v; even lanes work out m's
-        // step and odd lanes sqrt(v)'s
-        const bool odd = lane & 1;
-        if (av < 0x7F800000u) av = __float_as_uint(__fsqrt_rn(__uint_as_float(av)));
-        float d, inv;
-        block_step(odd ? av : am, odd ? float(kTopW * kTopW) : float(kTopM * kTopM), d, inv);
-        dm = __shfl_sync(0xffffffffu, d, 0);
-        dv = __shfl_sync(0xffffffffu, d, 1);
-        encode8<true>(m, nullptr, __shfl_sync(0xffffffffu, inv, 0), cm);
-        encode8<false>(v, w, __shfl_sync(0xffffffffu, inv, 1), cv);
-        store_codes<kFull>(c.m, i0, rem, lane, cm);
-        store_codes<kFull>(c.v, i0, rem, lane, cv);
-        if (lane == 0) {
-            reinterpret_cast<float *>(c.dm)[i0 / kBlock] = dm;
-            reinterpret_cast<float *>(c.dv)[i0 / kBlock] = dv;
-        }
+        for (int i = 0; i < 8; ++i) w[i] = sqrt_approx<true>(v[i]);
     } else {
-        store8<kFull>(c.m, false, i0, rem, lane, m);
-        store8<kFull>(c.v, false, i0, rem, lane, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = sqrt_approx<false>(v[i]);
     }
 }
-template <bool kState8, bool kPBf16, bool kGBf16>
-__device__ __forceinline__ void step_chunk(const StepArgs &a, const View &c, const Scalars &s, int lane) {
-    int i0 = 0;
-    for (; i0 + kBlock <= c.n; i0 += kBlock) step_block<kState8, kPBf16, kGBf16, true>(a, c, s, i0, kBlock, lane);
-    if (i0 < c.n) step_block<kState8, kPBf16, kGBf16, false>(a, c, s, i0, c.n - i0, lane);
-}
-template <bool kState8>
-__device__ __forceinline__ void step_types(const StepArgs &a, const View &c, const Scalars &s, int lane) {
-    switch (c.flags & (kParamBf16 | kGradBf16)) {
-        case 0: step_chunk<kState8, false, false>(a, c, s, lane); break;
-        case kParamBf16: step_chunk<kState8, true, false>(a, c, s, lane); break;
-        case kGradBf16: step_chunk<kState8, false, true>(a, c, s, lane); break;
-        default: step_chunk<kState8, true, true>(a, c, s, lane);
-    }
+__device__ __forceinline__ uint64_t update(const Scalars &s, float lr, float decay, uint64_t p, uint64_t m, float w0, float w1) {
+    float d0, d1;
+    unpack2(fma2(pack2(w0, w1), pack2(s.ds, s.ds), pack2(s.de, s.de)), d0, d1);
+    const uint64_t u = mul2(m, pack2(rcp_approx(d0), rcp_approx(d1)));
+    return fma2(pack2(-lr, -lr), fma2(pack2(decay, decay), p, u), p);
 }
 
-// A warp takes every (warps of the grid)-th chunk, with the next chunk's 80 bytes already on
-// their way; no barrier and no shared memory in the loop.  kKinds: the states the plan holds,
-// kKind32 | kKind8.
-enum { kKind32 = 1, kKind8 = 2 };
-constexpr int kCtas32 = 4, kCtas8 = 3;      // CTAs per SM that the registers are capped for
-template <int kKinds>
-__global__ void __launch_bounds__(kThreads, kKinds == kKind32 ? kCtas32 : kCtas8) adamw_kernel(const StepArgs a) {
-    __shared__ float s_bc[2];
+// ---- 32-bit states: 30 bytes per fp32 parameter, bound by HBM.
+template <bool kPBf16, bool kGBf16, bool kFull>
+__device__ __forceinline__ void step32_block(const StepArgs &a, const Scalars &s, const Chunk &c, int i0, int rem, int lane) {
+    Raw8<kGBf16> g;
+    Raw8<kPBf16> p;
+    Raw8<false> m, v;
+    m.template load<kFull>(c.m, i0, rem, lane);
+    v.template load<kFull>(c.v, i0, rem, lane);
+    g.template load<kFull>(c.g, i0, rem, lane);
+    p.template load<kFull>(c.p, i0, rem, lane);
+    float mf[8], vf[8], w[8], pf[8];
+    uint64_t mp[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint64_t vp = v.pair(i);
+        mp[i] = m.pair(i);
+        moments(a, s, g.pair(i), mp[i], vp);
+        unpack2(mp[i], mf[2 * i], mf[2 * i + 1]);
+        unpack2(vp, vf[2 * i], vf[2 * i + 1]);
+    }
+    roots(s, vf, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        unpack2(update(s, s.lr * c.lr_scale, c.decay, p.pair(i), mp[i], w[2 * i], w[2 * i + 1]), pf[2 * i], pf[2 * i + 1]);
+    store8<kFull>(c.p, kPBf16, i0, rem, lane, pf);
+    if (!kPBf16 && c.copy) store8<kFull>(c.copy, true, i0, rem, lane, pf);
+    store8<kFull>(c.m, false, i0, rem, lane, mf);
+    store8<kFull>(c.v, false, i0, rem, lane, vf);
+}
+template <bool kPBf16, bool kGBf16>
+__device__ __forceinline__ void step32_chunk(const StepArgs &a, const Scalars &s, const Chunk &c, int lane) {
+    int i0 = 0;
+    for (; i0 + kBlock <= c.n; i0 += kBlock) step32_block<kPBf16, kGBf16, true>(a, s, c, i0, kBlock, lane);
+    if (i0 < c.n) step32_block<kPBf16, kGBf16, false>(a, s, c, i0, c.n - i0, lane);
+}
+// A warp takes one chunk, and the CTAs come in the order of the list: what is read and written at any time
+// lies close together, which HBM rewards (a grid of four CTAs per SM that strides over the list took 631 us
+// where this takes 583, on 129 M fp32 parameters with bf16 copies).
+__global__ void __launch_bounds__(kThreads, 4) adamw32_kernel(const StepArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t nw = int64_t(gridDim.x) * kWarps;
-    int64_t i = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int64_t i = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
     // the chunk list was complete when the plan's call returned: it may be read before the wait
-    uint32_t word = i < a.nchunks ? chunk_word(a.chunks, i, lane) : 0u;
+    const uint32_t word = i < a.nchunks ? chunk_word(a.chunks, i, lane) : 0u;
     pdl_launch_dependents();
     pdl_wait();
     Scalars s;
-    s.coef = a.coef ? __ldcg(a.coef) : 1.f;          // a product with 1 changes nothing
-    if (!isfinite(s.coef)) return;                   // the gradients held an infinity or a NaN: nothing changes
-    const float lr = a.lr_dev ? __ldcg(a.lr_dev) : a.lr;
-    s.ds = a.ds;
-    s.de = a.de;
-    if (a.step_dev) {
-        if (threadIdx.x == 0) {
-            const int64_t t = *a.step_dev + 1;
-            const double bc1 = 1.0 - pow_int(a.beta1, t);
-            s_bc[0] = static_cast<float>(bc1 / sqrt(1.0 - pow_int(a.beta2, t)));
-            s_bc[1] = static_cast<float>(bc1 * a.eps);
-        }
-        __syncthreads();
-        s.ds = s_bc[0];
-        s.de = s_bc[1];
+    if (!read_scalars(a, s) || i >= a.nchunks) return;
+    Chunk c;
+    c.p = word64(word, 0), c.copy = word64(word, 2), c.g = word64(word, 4), c.m = word64(word, 6), c.v = word64(word, 8);
+    c.n = static_cast<int>(word32(word, 14)), c.flags = word32(word, 15);
+    c.lr_scale = __uint_as_float(word32(word, 16)), c.decay = __uint_as_float(word32(word, 17));
+    switch (c.flags & (kParamBf16 | kGradBf16)) {
+        case 0: step32_chunk<false, false>(a, s, c, lane); break;
+        case kParamBf16: step32_chunk<true, false>(a, s, c, lane); break;
+        case kGradBf16: step32_chunk<false, true>(a, s, c, lane); break;
+        default: step32_chunk<true, true>(a, s, c, lane);
     }
-    for (; i < a.nchunks; i += nw) {
-        const View c = view_of(word, lr);
-        if (i + nw < a.nchunks) word = chunk_word(a.chunks, i + nw, lane);
-        if (kKinds == kKind32 || (kKinds != kKind8 && !(c.flags & kState8))) step_types<false>(a, c, s, lane);
-        else step_types<true>(a, c, s, lane);
+}
+
+// ---- 8-bit states: 10 to 18 bytes per parameter.  The codes cost about 45 instructions per parameter, so
+// instruction issue and HBM take about equally long, and a block's dependent chain (absmax, division, root,
+// code) is as long as a load.  So each warp streams its blocks through a ring of three in shared memory by
+// asynchronous copies, two blocks ahead of the one it works on.  A lane copies exactly what it reads
+// back itself, so the ring needs no barrier; copies past a tensor's end are zero-filled.
+constexpr int kStages = 3;
+constexpr int kStageBytes = kBlock * (4 + 4 + 1 + 1);      // g, p, m, v
+constexpr int kSlots = 4;                                  // chunks between the block worked on and the one copied
+constexpr int kStep8Smem = kWarps * (kStages * kStageBytes + kSlots * int(sizeof(Chunk)));
+
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, uint64_t src, int bytes) {
+    if (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else if (kBytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// a lane's two runs of four elements (kSize bytes each) of the block at i0
+template <int kSize>
+__device__ __forceinline__ void copy_runs(uint32_t dst, uint64_t base, int i0, int rem, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int e = h * 128 + lane * 4;
+        copy_async<4 * kSize>(dst + e * kSize, base + uint64_t(i0 + e) * kSize, kSize * min(max(rem - e, 0), 4));
     }
-    if (a.step_dev) {
-        // the last CTA to get here counts the step: every CTA has read the counter by then
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            __threadfence();
-            if (atomicAdd(&a.head->ticket, 1u) == gridDim.x - 1) {
-                a.head->ticket = 0;
-                *a.step_dev += 1;
+}
+__device__ __forceinline__ void copy_block(const Chunk &c, uint32_t stage, int i0, int lane) {
+    const int rem = c.n - i0;
+    if (c.flags & kGradBf16) copy_runs<2>(stage, c.g, i0, rem, lane);
+    else copy_runs<4>(stage, c.g, i0, rem, lane);
+    if (c.flags & kParamBf16) copy_runs<2>(stage + 4 * kBlock, c.p, i0, rem, lane);
+    else copy_runs<4>(stage + 4 * kBlock, c.p, i0, rem, lane);
+    copy_runs<1>(stage + 8 * kBlock, c.m, i0, rem, lane);
+    copy_runs<1>(stage + 9 * kBlock, c.v, i0, rem, lane);
+}
+// pair i (of 4) of a lane's elements of a parameter or gradient in a stage
+template <bool kBf16>
+__device__ __forceinline__ uint64_t stage_pair(const uint8_t *base, int i, int lane) {
+    const int e = (i >> 1) * 128 + lane * 4 + 2 * (i & 1);
+    if (kBf16) {
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(base + 2 * e);
+        return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    }
+    return *reinterpret_cast<const uint64_t *>(base + 4 * e);
+}
+
+template <bool kPBf16, bool kGBf16, bool kFull>
+__device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s, const Chunk &c, const uint8_t *stage, float dm,
+                                            float dv, int i0, int lane) {
+    const int rem = c.n - i0;
+    float mf[8], vf[8], w[8], pf[8];
+    uint64_t m[4], v[4];
+    uint32_t cm[2], cv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        cm[h] = *reinterpret_cast<const uint32_t *>(stage + 8 * kBlock + h * 128 + lane * 4);
+        cv[h] = *reinterpret_cast<const uint32_t *>(stage + 9 * kBlock + h * 128 + lane * 4);
+    }
+    decode8<false>(cm, dm, m);
+    decode8<true>(cv, dv, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        moments(a, s, stage_pair<kGBf16>(stage, i, lane), m[i], v[i]);
+        unpack2(m[i], mf[2 * i], mf[2 * i + 1]);
+        unpack2(v[i], vf[2 * i], vf[2 * i + 1]);
+    }
+    roots(s, vf, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        unpack2(update(s, s.lr * c.lr_scale, c.decay, stage_pair<kPBf16>(stage + 4 * kBlock, i, lane), m[i], w[2 * i], w[2 * i + 1]),
+                pf[2 * i], pf[2 * i + 1]);
+    store8<kFull>(c.p, kPBf16, i0, rem, lane, pf);
+    if (!kPBf16 && c.copy) store8<kFull>(c.copy, true, i0, rem, lane, pf);
+    float am = 0.f, av = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // places past a tensor's end take no part in its last block's largest value
+        if (!kFull && (i >> 2) * 128 + lane * 4 + (i & 3) >= rem) mf[i] = vf[i] = w[i] = 0.f;
+        am = max_nan(am, mf[i]);
+        av = max_nan(av, vf[i]);
+    }
+    am = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(am)));
+    av = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(av)));
+    // the root is monotonic, so the largest root is the root of the largest v; even lanes work out m's
+    // step and odd lanes sqrt(v)'s
+    const bool odd = lane & 1;
+    float d, inv;
+    block_step(odd ? __fsqrt_rn(av) : am, odd ? float(kTopW * kTopW) : float(kTopM * kTopM), d, inv);
+    encode8<false>(mf, nullptr, __shfl_sync(0xffffffffu, inv, 0), false, cm);
+    // below 2^-92 a flushed root could have had a code above 0
+    encode8<true>(vf, w, __shfl_sync(0xffffffffu, inv, 1), s.flush && av < 2.0194839e-28f, cv);
+    store_codes<kFull>(c.m, i0, rem, lane, cm);
+    store_codes<kFull>(c.v, i0, rem, lane, cv);
+    if (lane < 2) reinterpret_cast<float *>(lane ? c.dv : c.dm)[i0 / kBlock] = d;
+}
+template <bool kPBf16, bool kGBf16>
+__device__ __forceinline__ void step8_any(const StepArgs &a, const Scalars &s, const Chunk &c, const uint8_t *stage, float dm,
+                                          float dv, int i0, int lane) {
+    if (c.n - i0 >= kBlock) step8_block<kPBf16, kGBf16, true>(a, s, c, stage, dm, dv, i0, lane);
+    else step8_block<kPBf16, kGBf16, false>(a, s, c, stage, dm, dv, i0, lane);
+}
+
+constexpr int kCtas8 = 3;      // CTAs per SM that the registers are capped for
+__global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const StepArgs a) {
+    extern __shared__ __align__(16) uint8_t step8_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint8_t *ring = step8_smem + warp * (kStages * kStageBytes);
+    Chunk *slots = reinterpret_cast<Chunk *>(step8_smem + kWarps * kStages * kStageBytes) + warp * kSlots;
+    const uint32_t ring_at = smem_u32(ring);
+    const int64_t stride = int64_t(gridDim.x) * kWarps;
+    int64_t done = int64_t(blockIdx.x) * kWarps + warp;       // the chunk worked on
+    if (done >= a.nchunks) return;
+    // the chunk list was complete when the plan's call returned: it may be read before the wait
+    int64_t ahead = done;                                     // the chunk copied from
+    if (lane < 20) reinterpret_cast<uint32_t *>(slots)[lane] = chunk_word(a.chunks, ahead, lane);
+    uint32_t word = ahead + stride < a.nchunks ? chunk_word(a.chunks, ahead + stride, lane) : 0u;
+    __syncwarp();
+    pdl_launch_dependents();
+    pdl_wait();
+    Scalars s;
+    if (!read_scalars(a, s)) return;
+    int to_slot = 0, to_i0 = 0, to_stage = 0;
+    float next_dm = 0.f, next_dv = 0.f;
+    // starts the copies of the next block of the list, if there is one; every call closes one group
+    auto copy_next = [&]() {
+        if (ahead < a.nchunks) {
+            const Chunk &c = slots[to_slot];
+            copy_block(c, ring_at + to_stage * kStageBytes, to_i0, lane);
+            to_i0 += kBlock;
+            if (to_i0 >= c.n) {
+                to_i0 = 0;
+                ahead += stride;
+                to_slot = (to_slot + 1) % kSlots;
+                __syncwarp();
+                if (lane < 20) reinterpret_cast<uint32_t *>(slots + to_slot)[lane] = word;
+                __syncwarp();
+                if (ahead + stride < a.nchunks) word = chunk_word(a.chunks, ahead + stride, lane);
             }
         }
+        to_stage = (to_stage + 1) % kStages;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto steps_of = [&](const Chunk &c, int i0) {
+        next_dm = reinterpret_cast<const float *>(c.dm)[i0 / kBlock];
+        next_dv = reinterpret_cast<const float *>(c.dv)[i0 / kBlock];
+    };
+    copy_next();
+    copy_next();
+    int slot = 0, stage = 0, i0 = 0;
+    steps_of(slots[0], 0);
+    while (true) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        copy_next();
+        const Chunk &c = slots[slot];
+        const float dm = next_dm, dv = next_dv;
+        // the block after this one
+        int n_slot = slot, n_i0 = i0 + kBlock;
+        if (n_i0 >= c.n) {
+            n_i0 = 0;
+            n_slot = (slot + 1) % kSlots;
+            done += stride;
+        }
+        if (done < a.nchunks) steps_of(slots[n_slot], n_i0);
+        const uint8_t *at = ring + stage * kStageBytes;
+        switch (c.flags & (kParamBf16 | kGradBf16)) {
+            case 0: step8_any<false, false>(a, s, c, at, dm, dv, i0, lane); break;
+            case kParamBf16: step8_any<true, false>(a, s, c, at, dm, dv, i0, lane); break;
+            case kGradBf16: step8_any<false, true>(a, s, c, at, dm, dv, i0, lane); break;
+            default: step8_any<true, true>(a, s, c, at, dm, dv, i0, lane);
+        }
+        if (done >= a.nchunks) return;
+        stage = (stage + 1) % kStages;
+        slot = n_slot;
+        i0 = n_i0;
     }
 }
 
 // Sum of squares of every gradient: each lane sums in double (a float32 square overflows at
 // 1.8e19 and loses what lies below 1e-19), each CTA leaves one partial sum, and the last CTA
-// adds the partials in a fixed order.  Chunks are dealt to warps by index, so the result
-// depends on the plan and the number of SMs only.
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Chunk *chunks, PlanHead *head, int64_t nchunks,
+// adds the partials in a fixed order.  CTA b takes the chunks [8 per_warp b, 8 per_warp (b + 1)), warp by
+// warp in turn: the result depends on the plan only, and the CTAs read in the order of the list (as in
+// adamw32_kernel).
+template <bool kBf16>
+__device__ __forceinline__ double sum_squares(const uint32_t *w, double sum) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float g = kBf16 ? __uint_as_float((i & 1) ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16) : __uint_as_float(w[i]);
+        sum = fma(double(g), double(g), sum);
+    }
+    return sum;
+}
+template <bool kBf16>
+__device__ __forceinline__ double norm_chunk(uint64_t g, int n, int lane, double sum) {
+    int i0 = 0;
+    for (; i0 + 2 * kBlock <= n; i0 += 2 * kBlock) {
+        Raw8<kBf16> x, y;
+        x.template load<true>(g, i0, kBlock, lane);
+        y.template load<true>(g, i0 + kBlock, kBlock, lane);
+        sum = sum_squares<kBf16>(x.w, sum);
+        sum = sum_squares<kBf16>(y.w, sum);
+    }
+    for (; i0 < n; i0 += kBlock) {
+        Raw8<kBf16> x;
+        x.template load<false>(g, i0, n - i0, lane);
+        sum = sum_squares<kBf16>(x.w, sum);
+    }
+    return sum;
+}
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Chunk *chunks, PlanHead *head, int64_t nchunks, int per_warp,
                                                              float max_norm, float *out) {
     __shared__ double s_sum[kWarps];
     __shared__ bool s_last;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t nw = int64_t(gridDim.x) * kWarps;
-    int64_t c = int64_t(blockIdx.x) * kWarps + warp;
-    uint32_t word = c < nchunks ? chunk_word(chunks, c, lane) : 0u;
+    const int64_t first = int64_t(blockIdx.x) * kWarps * per_warp + warp;
+    uint32_t word = first < nchunks ? chunk_word(chunks, first, lane) : 0u;
     pdl_launch_dependents();
     pdl_wait();
     double sum = 0.0;
-    for (; c < nchunks; c += nw) {
-        const uint64_t G = word64(word, 4);
+    for (int j = 0; j < per_warp && first + j * kWarps < nchunks; ++j) {
+        const uint64_t g = word64(word, 4);
         const int n = static_cast<int>(word32(word, 14));
         const bool bf16 = (word32(word, 15) & kGradBf16) != 0;
-        if (c + nw < nchunks) word = chunk_word(chunks, c + nw, lane);
-        for (int i0 = 0; i0 < n; i0 += kBlock) {
-            float g[8];
-            if (n - i0 >= kBlock) load8<true>(G, bf16, i0, n - i0, lane, g);
-            else load8<false>(G, bf16, i0, n - i0, lane, g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fma(double(g[i]), double(g[i]), sum);
-        }
+        if (j + 1 < per_warp && first + (j + 1) * kWarps < nchunks) word = chunk_word(chunks, first + (j + 1) * kWarps, lane);
+        sum = bf16 ? norm_chunk<true>(g, n, lane, sum) : norm_chunk<false>(g, n, lane, sum);
     }
     auto block_sum = [&](double x) {   // the sum of all threads' x, in thread 0
 #pragma unroll
@@ -472,19 +705,20 @@ __global__ void __launch_bounds__(kThreads) adam8_encode_kernel(const float *x, 
         float f[8];
         if (rem == kBlock) load8<true>(src, false, b * kBlock, rem, lane, f);
         else load8<false>(src, false, b * kBlock, rem, lane, f);
-        uint32_t c[2], top = 0;
-        float w[8], d, inv;
+        uint32_t c[2];
+        float w[8], top = 0.f, d, inv;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (kSecond) f[i] += 0.f;                       // -0 becomes 0
-            // a negative v has no root: its sign bit puts it above infinity here, with the NaNs
-            top = max(top, __float_as_uint(f[i]) & (kSecond ? 0xFFFFFFFFu : 0x7FFFFFFFu));
-            w[i] = sqrt_approx<false>(f[i]);
+            w[i] = 0.f;
+            if (kSecond) {
+                w[i] = sqrt_approx<false>(f[i]);
+                if (!(f[i] >= 0.f)) top = __uint_as_float(0x7FC00000u);   // a negative v has no root, like a NaN
+            }
+            top = max_nan(top, f[i]);
         }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (kSecond && top < 0x7F800000u) top = __float_as_uint(__fsqrt_rn(__uint_as_float(top)));
-        block_step(top, kSecond ? float(kTopW * kTopW) : float(kTopM * kTopM), d, inv);
-        encode8<!kSecond>(f, w, inv, c);
+        top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+        block_step(kSecond ? __fsqrt_rn(top) : top, kSecond ? float(kTopW * kTopW) : float(kTopM * kTopM), d, inv);
+        encode8<kSecond>(f, w, inv, false, c);
         if (rem == kBlock) store_codes<true>(dst, b * kBlock, rem, lane, c);
         else store_codes<false>(dst, b * kBlock, rem, lane, c);
         if (lane == 0) steps[b] = d;
@@ -502,12 +736,11 @@ __global__ void __launch_bounds__(kThreads) adam8_decode_kernel(const uint8_t *c
         uint32_t c[2];
         if (rem == kBlock) load_codes<true>(src, b * kBlock, rem, lane, c);
         else load_codes<false>(src, b * kBlock, rem, lane, c);
+        uint64_t y[4];
         float f[8];
-        decode8<!kSecond>(c, __ldcg(steps + b), f);
-        if (kSecond) {
+        decode8<kSecond>(c, __ldcg(steps + b), y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __fmul_rn(f[i], f[i]);
-        }
+        for (int i = 0; i < 4; ++i) unpack2(y[i], f[2 * i], f[2 * i + 1]);
         if (rem == kBlock) store8<true>(dst, false, b * kBlock, rem, lane, f);
         else store8<false>(dst, false, b * kBlock, rem, lane, f);
     }

@@ -1058,7 +1058,8 @@ static int embed_chunk(int64_t T, int64_t H) {
 
 size_t qlora_embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t H) {
     if (T < 0 || V <= 0 || H <= 0 || T > INT32_MAX || V > INT32_MAX || H > INT32_MAX || H % 8) return 0;
-    return std::max<size_t>(256, 4 * round256(size_t(T) * 4) + size_t(ceil_div(T, embed_chunk(T, H))) * 2 * size_t(H) * 4);
+    return 4 * round256(size_t(T) * 4) + round256(size_t(ceil_div(V, 32)) * 4) +
+           size_t(ceil_div(T, embed_chunk(T, H))) * 2 * size_t(H) * 4;
 }
 
 qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const void *dY, int dy_is_bf16, int64_t V,
@@ -1080,12 +1081,13 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
     a.H = H;
     a.pad = padding_id;
     uint8_t *wsb = static_cast<uint8_t *>(ws);
-    const size_t list = round256(size_t(T) * 4);
+    const size_t list = round256(size_t(T) * 4), mask = round256(size_t(ceil_div(V, 32)) * 4);
     for (int i = 0; i < 2; ++i) {
         a.key[i] = reinterpret_cast<uint32_t *>(wsb + list * i);
         a.pos[i] = reinterpret_cast<uint32_t *>(wsb + list * (2 + i));
     }
-    a.part = reinterpret_cast<float *>(wsb + 4 * list);
+    a.named = reinterpret_cast<uint32_t *>(wsb + 4 * list);
+    a.part = reinterpret_cast<float *>(wsb + 4 * list + mask);
     int nbits = 1;                                   // of the largest key, V
     while ((V >> nbits) != 0) ++nbits;
     a.passes = static_cast<int>(ceil_div(nbits, emb::kMaxBits));
@@ -1118,9 +1120,12 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
                               dim3(static_cast<unsigned>(ceil_div(a.nchunks - 1, emb::kJoinWarps)), static_cast<unsigned>(jtiles)),
                               emb::kJoinWarps * 32, 0, st, a));
     }
-    if (!accumulate)
-        QL_TRY(launch_pdl("embed_zero_kernel launch", emb::embed_zero_kernel, dim3(static_cast<unsigned>(2 * sm_count())),
-                          emb::kZeroThreads, 0, st, a, int(T == 0)));
+    if (!accumulate) {
+        // rows of about 16 KB a CTA
+        a.zero_rows = static_cast<int>(std::min<int64_t>(V, std::max<int64_t>(1, 16384 / (H * (de_is_bf16 ? 2 : 4)))));
+        QL_TRY(launch_pdl("embed_zero_kernel launch", emb::embed_zero_kernel,
+                          dim3(static_cast<unsigned>(ceil_div(V, a.zero_rows))), emb::kZeroThreads, 0, st, a));
+    }
     return QLORA_OK;
 }
 
@@ -1130,7 +1135,6 @@ static_assert(sizeof(qlora_adamw_tensor) == 80 && offsetof(qlora_adamw_tensor, f
 static_assert(sizeof(qlora_adamw_plan) == 48, "ABI layout");
 constexpr int32_t kOptFlags = QLORA_OPT_PARAM_BF16 | QLORA_OPT_GRAD_BF16 | QLORA_OPT_STATE_8BIT | QLORA_OPT_GRAD_ONLY;
 constexpr int32_t kPlanMagic = 0x51504c4e;
-constexpr int32_t kPlanGradOnly = 4;   // beside optim::kKind32 and kKind8 in a plan's kinds
 
 // Elements of a plan's chunk for `numel` in all: the largest multiple of 256 from 256 to 1024 that still
 // gives every warp of the device (64 per SM) a chunk.  A chunk's 80 bytes are 0.3 to 0.8 % of the bytes
@@ -1200,28 +1204,34 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     if (cap != cudaStreamCaptureStatusNone) return fail(QLORA_ERR_ARG, "a plan cannot be made during stream capture");
     uint8_t *host = static_cast<uint8_t *>(std::calloc(1, need));
     if (!host) return fail(QLORA_ERR_ARG, "no host memory for the plan (%zu bytes)", need);
-    optim::Chunk *c = reinterpret_cast<optim::Chunk *>(host + sizeof(optim::PlanHead));
-    int32_t kinds = 0;
-    for (int64_t i = 0; i < count; ++i) {
-        const qlora_adamw_tensor &t = tensors[i];
-        const bool only = (t.flags & QLORA_OPT_GRAD_ONLY) != 0, eight = (t.flags & QLORA_OPT_STATE_8BIT) != 0;
-        if (t.numel) kinds |= only ? kPlanGradOnly : eight ? optim::kKind8 : optim::kKind32;
-        const int64_t pb = (t.flags & QLORA_OPT_PARAM_BF16) ? 2 : 4, gb = (t.flags & QLORA_OPT_GRAD_BF16) ? 2 : 4, sb = eight ? 1 : 4;
-        auto at = [](const void *base, int64_t off) { return base ? uint64_t(reinterpret_cast<uintptr_t>(base)) + uint64_t(off) : 0; };
-        for (int64_t e = 0; e < t.numel; e += chunk, ++c) {
-            c->g = at(t.grad, e * gb);
-            c->n = static_cast<int32_t>(std::min(chunk, t.numel - e));
-            c->flags = uint32_t(t.flags) & (optim::kParamBf16 | optim::kGradBf16 | optim::kState8);
-            if (only) continue;
-            c->p = at(t.param, e * pb);
-            c->copy = at(t.param_bf16, e * 2);
-            c->m = at(t.exp_avg, e * sb);
-            c->v = at(t.exp_avg_sq, e * sb);
-            c->dm = eight ? at(t.exp_avg_step, e / optim::kBlock * 4) : 0;
-            c->dv = eight ? at(t.exp_avg_sq_step, e / optim::kBlock * 4) : 0;
-            c->lr_scale = t.lr_scale;
-            c->decay = t.weight_decay;
+    // chunks of tensors with 32-bit states first, then those with 8-bit states: a kernel for each
+    optim::Chunk *const list = reinterpret_cast<optim::Chunk *>(host + sizeof(optim::PlanHead)), *c = list;
+    int64_t chunks32 = 0;
+    int32_t grad_only = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int64_t i = 0; i < count; ++i) {
+            const qlora_adamw_tensor &t = tensors[i];
+            const bool only = (t.flags & QLORA_OPT_GRAD_ONLY) != 0, eight = !only && (t.flags & QLORA_OPT_STATE_8BIT) != 0;
+            if (eight != (pass == 1)) continue;
+            if (only && t.numel) grad_only = 1;
+            const int64_t pb = (t.flags & QLORA_OPT_PARAM_BF16) ? 2 : 4, gb = (t.flags & QLORA_OPT_GRAD_BF16) ? 2 : 4, sb = eight ? 1 : 4;
+            auto at = [](const void *base, int64_t off) { return base ? uint64_t(reinterpret_cast<uintptr_t>(base)) + uint64_t(off) : 0; };
+            for (int64_t e = 0; e < t.numel; e += chunk, ++c) {
+                c->g = at(t.grad, e * gb);
+                c->n = static_cast<int32_t>(std::min(chunk, t.numel - e));
+                c->flags = uint32_t(t.flags) & (optim::kParamBf16 | optim::kGradBf16);
+                if (only) continue;
+                c->p = at(t.param, e * pb);
+                c->copy = at(t.param_bf16, e * 2);
+                c->m = at(t.exp_avg, e * sb);
+                c->v = at(t.exp_avg_sq, e * sb);
+                c->dm = eight ? at(t.exp_avg_step, e / optim::kBlock * 4) : 0;
+                c->dv = eight ? at(t.exp_avg_sq_step, e / optim::kBlock * 4) : 0;
+                c->lr_scale = t.lr_scale;
+                c->decay = t.weight_decay;
+            }
         }
+        if (pass == 0) chunks32 = c - list;
     }
     cudaError_t e = cudaMemcpyAsync(buffer, host, need, cudaMemcpyHostToDevice, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
@@ -1229,9 +1239,9 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     QL_TRY(cuda_check(e, "copy of the plan"));
     plan->buffer = buffer;
     plan->chunks = nchunks;
-    plan->tensors = count;
+    plan->chunks32 = chunks32;
     plan->numel = numel;
-    plan->kinds = kinds;
+    plan->grad_only = grad_only;
     plan->magic = kPlanMagic;
     return QLORA_OK;
 }
@@ -1245,17 +1255,17 @@ static optim::PlanHead *plan_head(const qlora_adamw_plan *plan) { return static_
 static const optim::Chunk *plan_list(const qlora_adamw_plan *plan) {
     return reinterpret_cast<const optim::Chunk *>(plan_head(plan) + 1);
 }
-// CTAs of a pass over the plan's chunks: enough warps for every chunk, at most `per_sm` CTAs per SM
-static dim3 plan_grid(const qlora_adamw_plan *plan, int per_sm) {
+// CTAs for `chunks` chunks: a warp each, at most `per_sm` CTAs per SM
+static dim3 plan_grid(int64_t chunks, int per_sm) {
     return dim3(static_cast<unsigned>(std::max<int64_t>(
-        1, std::min<int64_t>({ceil_div(plan->chunks, optim::kWarps), int64_t(per_sm) * sm_count(), optim::kPartials}))));
+        1, std::min<int64_t>(ceil_div(chunks, optim::kWarps), int64_t(per_sm) * sm_count()))));
 }
 
 qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double beta1, double beta2, double eps,
                               int64_t step, const float *grad_scale, const float *lr_dev, int64_t *step_dev,
                               void *stream) {
     QL_TRY(check_plan(plan));
-    if (plan->kinds & kPlanGradOnly) return fail(QLORA_ERR_ARG, "the plan holds QLORA_OPT_GRAD_ONLY tensors");
+    if (plan->grad_only) return fail(QLORA_ERR_ARG, "the plan holds QLORA_OPT_GRAD_ONLY tensors");
     if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1)) return fail(QLORA_ERR_ARG, "betas must be in [0, 1)");
     if (!(eps >= 0) || !std::isfinite(eps)) return fail(QLORA_ERR_ARG, "eps must be finite and not negative");
     if (!lr_dev && !(lr >= 0 && std::isfinite(lr))) return fail(QLORA_ERR_ARG, "lr must be finite and not negative");
@@ -1264,37 +1274,40 @@ qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double be
     if ((reinterpret_cast<uintptr_t>(grad_scale) | reinterpret_cast<uintptr_t>(lr_dev)) & 3 || reinterpret_cast<uintptr_t>(step_dev) & 7)
         return fail(QLORA_ERR_ALIGN, "grad_scale, lr_dev and step_dev must be aligned to their types");
     QL_TRY(require_sm100());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
     optim::StepArgs a = {};
-    a.chunks = plan_list(plan);
     a.head = plan_head(plan);
     a.coef = grad_scale;
     a.lr_dev = lr_dev;
-    a.step_dev = step_dev;
-    a.beta1 = beta1;
-    a.beta2 = beta2;
-    a.eps = eps;
-    a.nchunks = plan->chunks;
     a.lr = lr_dev ? 0.f : static_cast<float>(lr);
+    a.one = 1.f;
     a.b1 = static_cast<float>(beta1);
     a.w1 = static_cast<float>(1.0 - beta1);
     a.b2 = static_cast<float>(beta2);
     a.w2 = static_cast<float>(1.0 - beta2);
-    if (!step_dev) {
+    if (step_dev) {
+        a.counted = 1;
+        QL_TRY(launch_pdl("step_scalars_kernel launch", optim::step_scalars_kernel, dim3(1), 1, 0, st, plan_head(plan), step_dev,
+                          grad_scale, beta1, beta2, eps));
+    } else {
         const double bc1 = 1.0 - std::pow(beta1, double(step));
         a.ds = static_cast<float>(bc1 / std::sqrt(1.0 - std::pow(beta2, double(step))));
         a.de = static_cast<float>(bc1 * eps);
     }
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const char *what = "adamw_kernel launch";
-    switch (plan->kinds) {
-        case optim::kKind32:
-            return launch_pdl(what, optim::adamw_kernel<optim::kKind32>, plan_grid(plan, optim::kCtas32), optim::kThreads, 0, st, a);
-        case optim::kKind8:
-            return launch_pdl(what, optim::adamw_kernel<optim::kKind8>, plan_grid(plan, optim::kCtas8), optim::kThreads, 0, st, a);
-        default:
-            return launch_pdl(what, optim::adamw_kernel<optim::kKind32 | optim::kKind8>, plan_grid(plan, optim::kCtas8),
-                              optim::kThreads, 0, st, a);
+    if (plan->chunks32 > 0) {
+        a.chunks = plan_list(plan);
+        a.nchunks = plan->chunks32;
+        QL_TRY(launch_pdl("adamw32_kernel launch", optim::adamw32_kernel,
+                          dim3(static_cast<unsigned>(ceil_div(a.nchunks, optim::kWarps))), optim::kThreads, 0, st, a));
     }
+    if (plan->chunks > plan->chunks32) {
+        a.chunks = plan_list(plan) + plan->chunks32;
+        a.nchunks = plan->chunks - plan->chunks32;
+        QL_TRY(set_smem(optim::adamw8_kernel, optim::kStep8Smem));
+        QL_TRY(launch_pdl("adamw8_kernel launch", optim::adamw8_kernel, plan_grid(a.nchunks, optim::kCtas8), optim::kThreads,
+                          optim::kStep8Smem, st, a));
+    }
+    return QLORA_OK;
 }
 
 qlora_status qlora_grad_norm(const qlora_adamw_plan *plan, float max_norm, float *out, void *stream) {
@@ -1303,8 +1316,12 @@ qlora_status qlora_grad_norm(const qlora_adamw_plan *plan, float max_norm, float
     if (!out) return fail(QLORA_ERR_ARG, "out is NULL");
     if (reinterpret_cast<uintptr_t>(out) & 3) return fail(QLORA_ERR_ALIGN, "out must be 4-byte aligned");
     QL_TRY(require_sm100());
-    return launch_pdl("grad_norm_kernel launch", optim::grad_norm_kernel, plan_grid(plan, 8), optim::kThreads, 0,
-                      static_cast<cudaStream_t>(stream), plan_list(plan), plan_head(plan), plan->chunks, max_norm, out);
+    const int64_t per_warp = std::max<int64_t>(1, ceil_div(plan->chunks, int64_t(optim::kWarps) * optim::kPartials));
+    if (per_warp > INT32_MAX) return fail(QLORA_ERR_SHAPE, "the plan is too large");
+    const int64_t grid = std::max<int64_t>(1, ceil_div(plan->chunks, optim::kWarps * per_warp));
+    return launch_pdl("grad_norm_kernel launch", optim::grad_norm_kernel, dim3(static_cast<unsigned>(grid)), optim::kThreads, 0,
+                      static_cast<cudaStream_t>(stream), plan_list(plan), plan_head(plan), plan->chunks, static_cast<int>(per_warp),
+                      max_norm, out);
 }
 
 static qlora_status check_adam8(const void *codes, int kind, const float *steps, const float *x, int64_t numel) {

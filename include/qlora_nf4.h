@@ -367,8 +367,8 @@ typedef struct {
  * by the calls below, opaque to the caller. */
 typedef struct {
     void *buffer;
-    int64_t chunks, tensors, numel;
-    int32_t kinds, magic;
+    int64_t chunks, chunks32, numel;
+    int32_t grad_only, magic;
     int64_t reserved;
 } qlora_adamw_plan;
 
