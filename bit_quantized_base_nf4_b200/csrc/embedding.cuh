@@ -37,27 +37,18 @@ struct FwdArgs {
     const uint16_t *d8;    // Q8_0
     Ids ids;
     void *out;
-    int64_t T, V, H;
+    int64_t T, V;
+    int H;
     float scale;
     int seg_shift;         // log2 of the row segments of kRun elements that a CTA takes (at most its warps)
+    int passes;            // tokens a warp takes, one after the other
     float level[16];
 };
 constexpr int kFwdThreads = 256;
 constexpr int kFwdWarps = kFwdThreads / 32;
 constexpr int kUnroll = 4;
 constexpr int kRun = 256 * kUnroll;   // elements of a row a warp takes: 8 per lane and step
-
-// scale words of the 64-weight run b64, as scale_load reads them
-__device__ __forceinline__ void scale_words(const ScaleSrc &s, int64_t b64, uint32_t &a, float &d) {
-    const int64_t b = b64 >> s.blk_shift;
-    if (s.dq) {
-        a = __ldcg(s.scales + b);
-        d = __ldcg(s.scales2 + (b >> 8));
-    } else {
-        a = __ldcg(reinterpret_cast<const uint32_t *>(s.scales) + b);
-        d = 1.f;
-    }
-}
+constexpr int kFwdPasses = 4;         // most tokens a warp takes
 
 // 32-bit words of 8 elements of a table
 template <int kTable>
@@ -66,121 +57,160 @@ __device__ __forceinline__ float level_at(const float *levels, uint32_t byte_off
     return *reinterpret_cast<const float *>(reinterpret_cast<const char *>(levels) + byte_offset);
 }
 
-// A warp takes one segment of one token's row: its id, then every code and scale load of the
-// segment at once, 8 elements per lane and step, so that a bf16 output is one 16-byte store.
-// CTAs: x over tokens, y over groups of 2^seg_shift segments.
-template <int kTable, bool kOutBf16>
-__global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const FwdArgs a) {
+// 8 elements from column e of a row on: as loaded (with the words of their scale), and as pairs of floats
+template <int kTable, bool kDq>
+struct Fetch {
+    uint32_t w[kWordsOf<kTable>];
+    uint32_t sa;
+    float sd;
+    // at: the place of the 8 elements in the table; off: 0, 256, 512 ... elements behind it
+    __device__ __forceinline__ void load(const FwdArgs &a, int64_t at, int off) {
+        if (kTable == kTableNf4) {
+            w[0] = __ldcg(reinterpret_cast<const uint32_t *>(static_cast<const uint8_t *>(a.table) + (at >> 1)) + off / 8);
+            const int64_t b = (at >> 6 >> a.sc.blk_shift) + (off / 64 >> a.sc.blk_shift);
+            if (kDq) {
+                sa = __ldcg(a.sc.scales + b);
+                sd = __ldcg(a.sc.scales2 + (b >> 8));
+            } else {
+                sa = __ldcg(reinterpret_cast<const uint32_t *>(a.sc.scales) + b);
+            }
+        } else if (kTable == kTableQ8) {
+            const uint2 q = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(a.table) + at) + off / 8);
+            w[0] = q.x;
+            w[1 % kWordsOf<kTable>] = q.y;
+            sa = __ldcg(a.d8 + (at >> 5) + off / 32);
+        } else {
+            const char *p = static_cast<const char *>(a.table) + at * (kTable == kTableBf16 ? 2 : 4);
+#pragma unroll
+            for (int h = 0; h < kWordsOf<kTable> / 4; ++h) {
+                const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(p) + off / (kTable == kTableBf16 ? 8 : 4) + h);
+                w[(4 * h) % kWordsOf<kTable>] = x.x, w[(4 * h + 1) % kWordsOf<kTable>] = x.y;
+                w[(4 * h + 2) % kWordsOf<kTable>] = x.z, w[(4 * h + 3) % kWordsOf<kTable>] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void values(const float *levels, uint64_t scale, uint64_t *y) const {
+        if (kTable == kTableNf4) {
+            // byte offsets 4 c into the level table, four codes at a time
+            const float f = kDq ? __fmul_rn(static_cast<float>(sa), sd) : __uint_as_float(sa);
+            const uint32_t lo = (w[0] << 2) & 0x3C3C3C3Cu, hi = (w[0] >> 2) & 0x3C3C3C3Cu;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                y[j] = mul2(pack2(level_at(levels, __byte_perm(lo, 0u, 0x4440u + j)), level_at(levels, __byte_perm(hi, 0u, 0x4440u + j))),
+                            pack2(f, f));
+        } else if (kTable == kTableQ8) {
+            const float f = __half2float(__ushort_as_half(static_cast<unsigned short>(sa)));
+            const uint64_t magic = pack2(-8388736.f, -8388736.f);   // -(2^23 + 128)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t b = w[(j / 2) % kWordsOf<kTable>] ^ 0x80808080u;
+                y[j] = mul2(add2(pack2(__uint_as_float(__byte_perm(b, 0x4B000000u, 0x7650 + 2 * (j & 1))),
+                                       __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7651 + 2 * (j & 1)))), magic), pack2(f, f));
+            }
+        } else if (kTable == kTableBf16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = w[j % kWordsOf<kTable>];
+                y[j] = pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                y[j] = pack2(__uint_as_float(w[(2 * j) % kWordsOf<kTable>]), __uint_as_float(w[(2 * j + 1) % kWordsOf<kTable>]));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = mul2(y[j], scale);
+    }
+};
+// 8 elements to a row of the output
+template <bool kOutBf16>
+__device__ __forceinline__ void put8(char *row, int e, const uint64_t *w) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpack2(w[j], y[2 * j], y[2 * j + 1]);
+    if (kOutBf16) {
+        uint32_t b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
+            b[j] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+        reinterpret_cast<uint4 *>(row)[e >> 3] = make_uint4(b[0], b[1], b[2], b[3]);
+    } else {
+        float4 *dst = reinterpret_cast<float4 *>(row) + (e >> 2);
+        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
+}
+
+// A warp takes one segment of a token's row: every code and scale load of the segment at once, 8 elements
+// per lane and step, so that a bf16 output is one 16-byte store.  Then the same segment of the CTA's next token.
+// CTAs: x over groups of tokens, in the order of the output; y over groups of 2^seg_shift segments.
+template <int kTable, bool kDq, bool kOutBf16>
+__global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const __grid_constant__ FwdArgs a) {
     __shared__ float s_lv[16];
     if (kTable == kTableNf4) {
-        float lv = 0.f;
-#pragma unroll
-        for (int l = 0; l < 16; ++l)
-            if ((threadIdx.x & 15) == l) lv = a.level[l];
-        if (threadIdx.x < 16) s_lv[threadIdx.x] = lv;
+        if (threadIdx.x < 16) s_lv[threadIdx.x] = a.level[threadIdx.x];
         __syncthreads();
     }
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = int64_t(blockIdx.x) * (kFwdWarps >> a.seg_shift) + (warp >> a.seg_shift);
-    const int64_t e0 = ((int64_t(blockIdx.y) << a.seg_shift) + (warp & ((1 << a.seg_shift) - 1))) * kRun + lane * 8;
-    if (t >= a.T) return;
-    const int64_t id = id_at(a.ids, t);
-    const bool ok = id >= 0 && id < a.V;
-    if (!ok && lane == 0) report_bad_id();
-    const int64_t row = ok ? id * a.H : 0;
-
-    uint32_t raw[kUnroll][kWordsOf<kTable>];
-    uint32_t sa[kUnroll];
-    float sd[kUnroll];
+    const int per_pass = kFwdWarps >> a.seg_shift;           // tokens of the CTA in one pass
+    const int64_t t0 = int64_t(blockIdx.x) * (per_pass * a.passes) + (warp >> a.seg_shift);
+    const int e0 = static_cast<int>((blockIdx.y << a.seg_shift) + (warp & ((1 << a.seg_shift) - 1))) * kRun + lane * 8;
+    if (e0 - lane * 8 >= a.H) return;
+    int64_t ids[kFwdPasses];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const int64_t e = e0 + u * 256;
-        if (e >= a.H || !ok) continue;
-        const int64_t at = row + e;
-        if (kTable == kTableNf4) {
-            raw[u][0] = __ldcg(reinterpret_cast<const uint32_t *>(a.table) + (at >> 3));
-            scale_words(a.sc, at >> 6, sa[u], sd[u]);
-        } else if (kTable == kTableQ8) {
-            const uint2 q = __ldcg(reinterpret_cast<const uint2 *>(a.table) + (at >> 3));
-            raw[u][0] = q.x;
-            raw[u][1 % kWordsOf<kTable>] = q.y;
-            sa[u] = __ldcg(a.d8 + (at >> 5));
-        } else {
-#pragma unroll
-            for (int h = 0; h < kWordsOf<kTable> / 4; ++h) {
-                const uint4 x = __ldcg(reinterpret_cast<const uint4 *>(static_cast<const char *>(a.table) + at * (kTable == kTableBf16 ? 2 : 4)) + h);
-                raw[u][(4 * h) % kWordsOf<kTable>] = x.x, raw[u][(4 * h + 1) % kWordsOf<kTable>] = x.y;
-                raw[u][(4 * h + 2) % kWordsOf<kTable>] = x.z, raw[u][(4 * h + 3) % kWordsOf<kTable>] = x.w;
-            }
-        }
-    }
+    for (int p = 0; p < kFwdPasses; ++p)
+        ids[p] = p < a.passes && t0 + p * per_pass < a.T ? id_at(a.ids, t0 + p * per_pass) : 0;
     const uint64_t scale = pack2(a.scale, a.scale);
+#pragma unroll 1
+    for (int p = 0; p < a.passes; ++p) {
+        const int64_t t = t0 + p * per_pass;
+        if (t >= a.T) return;
+        int64_t id = ids[0];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-        const int64_t e = e0 + u * 256;
-        if (e >= a.H) break;
-        uint64_t w[4] = {0, 0, 0, 0};              // pairs of elements
-        if (ok) {
-            if (kTable == kTableNf4) {
-                // byte offsets 4 c into the level table, four codes at a time; level(c) of two neighbours
-                const float f = scale_of(a.sc, sa[u], sd[u]);
-                const uint32_t lo = (raw[u][0] << 2) & 0x3C3C3C3Cu, hi = (raw[u][0] >> 2) & 0x3C3C3C3Cu;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = mul2(pack2(level_at(s_lv, __byte_perm(lo, 0u, 0x4440u + j)), level_at(s_lv, __byte_perm(hi, 0u, 0x4440u + j))),
-                                pack2(f, f));
-            } else if (kTable == kTableQ8) {
-                const float f = __half2float(__ushort_as_half(static_cast<unsigned short>(sa[u])));
-                const uint64_t magic = pack2(-8388736.f, -8388736.f);   // -(2^23 + 128)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t b = raw[u][(j / 2) % kWordsOf<kTable>] ^ 0x80808080u;
-                    w[j] = mul2(add2(pack2(__uint_as_float(__byte_perm(b, 0x4B000000u, 0x7650 + 2 * (j & 1))),
-                                           __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7651 + 2 * (j & 1)))), magic), pack2(f, f));
-                }
-            } else if (kTable == kTableBf16) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t x = raw[u][j % kWordsOf<kTable>];
-                    w[j] = pack2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = pack2(__uint_as_float(raw[u][(2 * j) % kWordsOf<kTable>]), __uint_as_float(raw[u][(2 * j + 1) % kWordsOf<kTable>]));
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = mul2(w[j], scale);
+        for (int j = 1; j < kFwdPasses; ++j) id = p == j ? ids[j] : id;
+        char *row = static_cast<char *>(a.out) + t * a.H * (kOutBf16 ? 2 : 4);
+        if (id < 0 || id >= a.V) {
+            if (lane == 0) report_bad_id();
+            const uint64_t zero[4] = {0, 0, 0, 0};
+            for (int e = e0; e < a.H && e < e0 + kRun; e += 256) put8<kOutBf16>(row, e, zero);
+            continue;
         }
-        float y[8];
+        const int64_t at = id * a.H + e0;
+        Fetch<kTable, kDq> x[kUnroll];
+        uint64_t y[4];
+        if (e0 - lane * 8 + kRun <= a.H) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) unpack2(w[j], y[2 * j], y[2 * j + 1]);
-        const int64_t o = t * a.H + e;
-        if (kOutBf16) {
-            uint32_t b[4];
+            for (int u = 0; u < kUnroll; ++u) x[u].load(a, at, u * 256);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(y[2 * j], y[2 * j + 1]);
-                b[j] = *reinterpret_cast<const uint32_t *>(&p);
+            for (int u = 0; u < kUnroll; ++u) {
+                x[u].values(s_lv, scale, y);
+                put8<kOutBf16>(row, e0 + u * 256, y);
             }
-            reinterpret_cast<uint4 *>(a.out)[o >> 3] = make_uint4(b[0], b[1], b[2], b[3]);
         } else {
-            float4 *dst = reinterpret_cast<float4 *>(a.out) + (o >> 2);
-            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (e0 + u * 256 < a.H) x[u].load(a, at, u * 256);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (e0 + u * 256 >= a.H) break;
+                x[u].values(s_lv, scale, y);
+                put8<kOutBf16>(row, e0 + u * 256, y);
+            }
         }
     }
 }
 
 // ------------------------------------------------------------------ gradient
 // dE[v, :] (+)= scale * sum over the tokens t with id_t = v of dY[t, :], in up to four launches:
-//   sort    the tokens by id (stable);
+//   sort    the tokens by id (stable), and mark the rows that they name;
 //   reduce  equal runs of `chunk` sorted tokens each: an id that lies wholly in a chunk is summed
 //           and written, one that crosses a border leaves a partial sum per chunk;
 //   join    adds the partial sums of each such id in order and writes its row;
-//   zero    (unless the gradient is added) zeroes the rows that no token names.
+//   zero    (unless the gradient is added) zeroes the other rows.
 // Every sum is float32, in an order fixed by the ids alone: results repeat bit for bit.
 // The last three overlap: each starts once the one before it has started (programmatic dependent
 // launch).  `zero` needs the sort only, so its writes, nearly all of the time when the table is large, run
@@ -236,11 +266,108 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t *p, uint32_t rank)
     return v;
 }
 
-// Radix sort by the cluster of blocks 0 .. kSortCtas - 1, least significant digit first.  Tokens are
-// dealt in order to CTAs, warps and rounds of 32, so a token's place among equal digits is the count
-// in lower CTAs, in lower warps, in its warp's earlier rounds and in its lower lanes: stable without
-// atomics.
-__device__ void sort_tokens(const GradArgs &a, uint32_t *smem) {
+// The first sweep's ranking: the place of a token among the equal digits that its warp has met so far.
+__device__ __forceinline__ uint32_t rank_digit(uint32_t *my, uint32_t d, bool in, int lane) {
+    const uint32_t same = __match_any_sync(0xffffffffu, in ? d : uint32_t(kMaxBins));   // idle lanes match none
+    const uint32_t lower = same & ((1u << lane) - 1u);
+    uint32_t r = 0;
+    if (in) r = my[d] + __popc(lower);
+    __syncwarp();
+    if (in && lower == 0) my[d] += __popc(same);
+    __syncwarp();
+    return r;
+}
+// Per bin: counts of lower warps in hist, the CTA's total as the result (threads below `bins`).
+__device__ __forceinline__ uint32_t scan_warps(uint32_t *hist, int bin) {
+    uint32_t sum = 0, n[kSortWarps];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) n[w] = hist[w * kMaxBins + bin];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) {
+        hist[w * kMaxBins + bin] = sum;
+        sum += n[w];
+    }
+    return sum;
+}
+// Exclusive scan over the CTA's threads of n; wsum holds kSortWarps words.
+__device__ __forceinline__ uint32_t scan_threads(uint32_t n, uint32_t *wsum, int warp, int lane) {
+    uint32_t incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    uint32_t base = lane < warp ? wsum[lane] : 0u;
+    base = __reduce_add_sync(0xffffffffu, base);
+    return base + incl - n;
+}
+
+// One CTA sorts up to 1024 kRounds tokens: keys and places in registers, exchanged through shared memory.
+// Tokens are dealt in order to warps and rounds of 32, so a token's place among equal digits is the count in
+// lower warps, in its warp's earlier rounds and in its lower lanes: stable without atomics.
+constexpr int kOneRounds = 16;
+constexpr int kOneTokens = kOneRounds * kSortThreads;
+constexpr int one_smem(int64_t T) { return kSortSmem + 8 * kSortThreads * int((T + kSortThreads - 1) / kSortThreads); }
+template <int kRounds>
+__device__ void sort_one(const GradArgs &a, uint32_t *smem) {
+    uint32_t *hist = smem, *first = hist + kSortWarps * kMaxBins, *wsum = first + 2 * kMaxBins;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = static_cast<int>(a.T);
+    const int rounds = (T + kSortThreads - 1) / kSortThreads;         // at most kRounds
+    uint32_t *keys = smem + kSortSmem / 4, *places = keys + rounds * kSortThreads;
+    const int i0 = warp * rounds * 32 + lane, bins = 1 << a.bits;
+    uint32_t *my = hist + warp * kMaxBins;
+    uint32_t k[kRounds], p[kRounds], r[kRounds];
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+        const int t = i0 + 32 * u;
+        k[u] = u < rounds && t < T ? key_of(a, t) : 0u;
+        p[u] = t;
+    }
+    if (!a.accumulate) {
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u)
+            if (u < rounds && i0 + 32 * u < T && k[u] < a.V) atomicOr(a.named + (k[u] >> 5), 1u << (k[u] & 31));
+    }
+    for (int pass = 0; pass < a.passes; ++pass) {
+        const int shift = pass * a.bits;
+        for (int b = lane; b < bins; b += 32) my[b] = 0;
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u)
+            if (u < rounds) r[u] = rank_digit(my, (k[u] >> shift) & (bins - 1), i0 + 32 * u < T, lane);
+        __syncthreads();
+        const uint32_t total = tid < bins ? scan_warps(hist, tid) : 0u;
+        const uint32_t base = scan_threads(total, wsum, warp, lane);
+        if (tid < bins) first[tid] = base;
+        __syncthreads();
+        const bool last = pass + 1 == a.passes;
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) {
+            if (u >= rounds || i0 + 32 * u >= T) continue;
+            const uint32_t d = (k[u] >> shift) & (bins - 1), at = first[d] + my[d] + r[u];
+            if (last) {
+                __stcg(a.key[a.passes & 1] + at, k[u]);
+                __stcg(a.pos[a.passes & 1] + at, p[u]);
+            } else {
+                keys[at] = k[u];
+                places[at] = p[u];
+            }
+        }
+        if (last) return;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) {
+            const int t = i0 + 32 * u;
+            if (u < rounds && t < T) k[u] = keys[t], p[u] = places[t];
+        }
+    }
+}
+
+// More tokens: the cluster of kSortCtas CTAs sorts with the same dealing over CTAs, warps and rounds; bins and
+// counts meet in shared memory of the cluster, tokens in global memory (L2), one digit after the other.
+__device__ void sort_cluster(const GradArgs &a, uint32_t *smem) {
     uint32_t *hist = smem;                               // [warp][bin]
     uint32_t *total = hist + kSortWarps * kMaxBins;      // [bin] of this CTA
     uint32_t *first = total + kMaxBins;                  // [bin] first place of this CTA's tokens
@@ -258,37 +385,30 @@ __device__ void sort_tokens(const GradArgs &a, uint32_t *smem) {
         const int shift = pass * a.bits;
         for (int b = lane; b < bins; b += 32) my[b] = 0;
         __syncwarp();
-        for (int64_t i = i_lo; i < i_hi; i += 32 * kSortBatch) {
-            uint32_t k[kSortBatch];
+        // two sweeps over the warp's tokens: count the digits, then place the tokens
+        auto sweep = [&](auto &&use) {
+            for (int64_t i = i_lo; i < i_hi; i += 32 * kSortBatch) {
+                uint32_t k[kSortBatch], p[kSortBatch];
 #pragma unroll
-            for (int u = 0; u < kSortBatch; ++u) {
-                const int64_t t = i + 32 * u + lane;
-                k[u] = t < i_hi ? (pass ? __ldcg(src_k + t) : key_of(a, t)) : 0u;
-            }
+                for (int u = 0; u < kSortBatch; ++u) {
+                    const int64_t t = i + 32 * u + lane;
+                    k[u] = t < i_hi ? (pass ? __ldcg(src_k + t) : key_of(a, t)) : 0u;
+                    p[u] = t < i_hi && pass ? __ldcg(src_p + t) : static_cast<uint32_t>(t);
+                }
 #pragma unroll
-            for (int u = 0; u < kSortBatch; ++u) {
-                if (i + 32 * u >= i_hi) break;
-                const bool in = i + 32 * u + lane < i_hi;
-                if (pass == 0 && !a.accumulate && in && k[u] < a.V) atomicOr(a.named + (k[u] >> 5), 1u << (k[u] & 31));
-                const uint32_t d = in ? (k[u] >> shift) & (bins - 1) : uint32_t(kMaxBins);   // idle lanes match none
-                const uint32_t same = __match_any_sync(0xffffffffu, d);
-                if (in && (same & ((1u << lane) - 1u)) == 0) my[d] += __popc(same);
-                __syncwarp();
+                for (int u = 0; u < kSortBatch; ++u) {
+                    if (i + 32 * u >= i_hi) break;
+                    const bool in = i + 32 * u + lane < i_hi;
+                    const uint32_t d = (k[u] >> shift) & (bins - 1);
+                    use(k[u], p[u], d, rank_digit(my, d, in, lane), in);
+                }
             }
-        }
+        };
+        sweep([&](uint32_t k, uint32_t, uint32_t, uint32_t, bool in) {
+            if (pass == 0 && !a.accumulate && in && k < a.V) atomicOr(a.named + (k >> 5), 1u << (k & 31));
+        });
         __syncthreads();
-        // per bin: counts of lower warps, and this CTA's total
-        if (tid < bins) {
-            uint32_t sum = 0, n[kSortWarps];
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) n[w] = hist[w * kMaxBins + tid];
-#pragma unroll
-            for (int w = 0; w < kSortWarps; ++w) {
-                hist[w * kMaxBins + tid] = sum;
-                sum += n[w];
-            }
-            total[tid] = sum;
-        }
+        if (tid < bins) total[tid] = scan_warps(hist, tid);
         cluster_barrier();
         uint32_t below = 0, all = 0;
         if (tid < bins) {
@@ -299,61 +419,42 @@ __device__ void sort_tokens(const GradArgs &a, uint32_t *smem) {
                 if (r < rank) below += n;
             }
         }
-        // exclusive scan of `all` over the bins (the first bins / 32 warps hold them)
-        uint32_t incl = all;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t n = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += n;
-        }
-        if (lane == 31) wsum[warp] = incl;
+        const uint32_t base = scan_threads(all, wsum, warp, lane);
+        if (tid < bins) first[tid] = base + below;
         __syncthreads();
-        if (tid < bins) {
-            uint32_t base = incl - all + below;
-            for (int w = 0; w < warp; ++w) base += wsum[w];
-            first[tid] = base;
-        }
-        __syncthreads();
-        for (int64_t i = i_lo; i < i_hi; i += 32 * kSortBatch) {
-            uint32_t k[kSortBatch], p[kSortBatch];
-#pragma unroll
-            for (int u = 0; u < kSortBatch; ++u) {
-                const int64_t t = i + 32 * u + lane;
-                k[u] = t < i_hi ? (pass ? __ldcg(src_k + t) : key_of(a, t)) : 0u;
-                p[u] = t < i_hi && pass ? __ldcg(src_p + t) : static_cast<uint32_t>(t);
+        // hist now counts on from the lower warps' numbers
+        sweep([&](uint32_t k, uint32_t p, uint32_t d, uint32_t r, bool in) {
+            if (in) {
+                const uint32_t at = first[d] + r;
+                __stcg(dst_k + at, k);
+                __stcg(dst_p + at, p);
             }
-#pragma unroll
-            for (int u = 0; u < kSortBatch; ++u) {
-                if (i + 32 * u >= i_hi) break;
-                const bool in = i + 32 * u + lane < i_hi;
-                const uint32_t d = in ? (k[u] >> shift) & (bins - 1) : uint32_t(kMaxBins);
-                const uint32_t same = __match_any_sync(0xffffffffu, d);
-                const uint32_t lower = same & ((1u << lane) - 1u);
-                uint32_t at = 0;
-                if (in) at = first[d] + my[d] + __popc(lower);
-                __syncwarp();
-                if (in && lower == 0) my[d] += __popc(same);
-                __syncwarp();
-                if (in) {
-                    __stcg(dst_k + at, k[u]);
-                    __stcg(dst_p + at, p[u]);
-                }
-            }
-        }
+        });
         cluster_barrier();   // the next pass reads what every CTA wrote; total is free again
     }
 }
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) embed_sort_kernel(const GradArgs a) {
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort_cluster_kernel(const GradArgs a) {
     extern __shared__ uint32_t sort_smem[];
     pdl_launch_dependents();
     pdl_wait();
-    if (!a.accumulate) {        // which rows are named; the marks are set by the sort's first pass
+    if (!a.accumulate) {        // no row is named yet; the sort's first pass marks them
         for (int64_t i = int64_t(cluster_rank()) * kSortThreads + threadIdx.x; i < (a.V + 31) / 32; i += kSortCtas * kSortThreads)
             __stcg(a.named + i, 0u);
         cluster_barrier();
     }
-    sort_tokens(a, sort_smem);
+    sort_cluster(a, sort_smem);
+}
+template <int kRounds>
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const GradArgs a) {
+    extern __shared__ uint32_t sort_smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    if (!a.accumulate) {
+        for (int64_t i = threadIdx.x; i < (a.V + 31) / 32; i += kSortThreads) __stcg(a.named + i, 0u);
+        __syncthreads();
+    }
+    sort_one<kRounds>(a, sort_smem);
 }
 
 // Zero: a CTA of 256 threads for about 16 KB of rows, in the order of the table.  (A grid of two CTAs per SM
@@ -502,24 +603,30 @@ __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArg
 // each over an equal part of the list, and the eight sums in order.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCols = 512;         // four runs of 128
-constexpr int kLongJoin = 32;
+constexpr int kLongJoin = 8;
 __device__ __forceinline__ void add4(float4 &s, const float4 x) {
     s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
 }
 __device__ __forceinline__ float4 load_part(const GradArgs &a, int64_t slot, int64_t c) {
     return __ldcg(reinterpret_cast<const float4 *>(a.part + slot * a.H + c));
 }
-// sum of the first-run partials of chunks [lo, hi), columns c .. c + 3, on top of s
-__device__ __forceinline__ float4 sum_firsts(const GradArgs &a, float4 s, int64_t lo, int64_t hi, int64_t c) {
-    for (; lo + 8 <= hi; lo += 8) {
-        float4 x[8];
+constexpr int kJoinRuns = kJoinCols / 128;
+// adds the first-run partials of chunks [lo, hi), columns c + 128 q .. + 3, to s[q]; two chunks in flight
+__device__ __forceinline__ void sum_firsts(const GradArgs &a, float4 *s, int64_t lo, int64_t hi, int64_t c) {
+    for (; lo < hi; lo += 2) {
+        float4 x[2][kJoinRuns];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = load_part(a, 2 * (lo + u), c);
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 8; ++u) add4(s, x[u]);
+            for (int q = 0; q < kJoinRuns; ++q) {
+                x[u][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (lo + u < hi && c + 128 * q < a.H) x[u][q] = load_part(a, 2 * (lo + u), c + 128 * q);
+            }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int q = 0; q < kJoinRuns; ++q) add4(s[q], x[u][q]);
     }
-    for (; lo < hi; ++lo) add4(s, load_part(a, 2 * lo, c));
-    return s;
 }
 // one past the last chunk that starts with id, given that chunk lo does: 32 chunks at a time over the
 // whole warp, the next 32 first (few ids go further), then 32 places spread over what is left
@@ -539,7 +646,7 @@ template <bool kDeBf16>
 __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradArgs a) {
     __shared__ int64_t s_end[kJoinWarps];
     __shared__ uint32_t s_id[kJoinWarps], s_slot[kJoinWarps];
-    __shared__ float4 s_part[kJoinWarps][32];
+    __shared__ float4 s_part[kJoinWarps][kJoinRuns][32];
     pdl_launch_dependents();
     pdl_wait();
     const uint32_t *ids = a.key[a.passes & 1];
@@ -559,17 +666,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradA
             end = end_of_id(a, ids, id, ch + 1, lane);
         }
     }
-    if (end && end - ch <= kLongJoin) {
+    // the id's row from the sums s of the columns c + 128 q, on top of its old values
+    auto finish = [&](uint32_t row, const float4 *s) {
+        Raw<kDeBf16, 4> old[kJoinRuns];
 #pragma unroll
-        for (int q = 0; q < kJoinCols / 128; ++q) {
-            const int64_t cq = c + 128 * q;
-            if (cq >= a.H) break;
-            Raw<kDeBf16, 4> old;
-            old.zero();
-            if (a.accumulate) old.load(a.dE, int64_t(id) * a.H + cq);
-            const float4 s = sum_firsts(a, load_part(a, 2 * ch + slot, cq), ch + 1, end, cq);
-            write_row<kDeBf16, 4>(a, id, cq, reinterpret_cast<const float *>(&s), old);
+        for (int q = 0; q < kJoinRuns; ++q) {
+            old[q].zero();
+            if (a.accumulate && c + 128 * q < a.H) old[q].load(a.dE, int64_t(row) * a.H + c + 128 * q);
         }
+#pragma unroll
+        for (int q = 0; q < kJoinRuns; ++q)
+            if (c + 128 * q < a.H) write_row<kDeBf16, 4>(a, row, c + 128 * q, reinterpret_cast<const float *>(s + q), old[q]);
+    };
+    auto start = [&](float4 *s, int64_t chunk, uint32_t which) {
+#pragma unroll
+        for (int q = 0; q < kJoinRuns; ++q) {
+            s[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (chunk >= 0 && c + 128 * q < a.H) s[q] = load_part(a, 2 * chunk + which, c + 128 * q);
+        }
+    };
+    float4 s[kJoinRuns];
+    if (end && end - ch <= kLongJoin) {
+        start(s, ch, slot);
+        sum_firsts(a, s, ch + 1, end, c);
+        finish(id, s);
     }
     if (lane == 0) {
         s_end[warp] = end && end - ch > kLongJoin ? end : 0;
@@ -580,24 +700,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embed_join_kernel(const GradA
     for (int w = 0; w < kJoinWarps; ++w) {
         if (!s_end[w]) continue;                                  // the same for the whole block
         const int64_t lo = ch - warp + w + 1, n = s_end[w] - lo;  // first-run partials of chunks [lo, lo + n)
-        for (int64_t cq = c; cq < c - lane * 4 + kJoinCols && cq - lane * 4 < a.H; cq += 128) {
-            Raw<kDeBf16, 4> old;
-            old.zero();
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (cq < a.H) {
-                if (warp == 0) s = load_part(a, 2 * (lo - 1) + s_slot[w], cq);
-                if (warp == 0 && a.accumulate) old.load(a.dE, int64_t(s_id[w]) * a.H + cq);
-                s = sum_firsts(a, s, lo + n * warp / kJoinWarps, lo + n * (warp + 1) / kJoinWarps, cq);
-            }
-            s_part[warp][lane] = s;
-            __syncthreads();
-            if (warp == 0 && cq < a.H) {
+        start(s, warp == 0 ? lo - 1 : -1, s_slot[w]);
+        sum_firsts(a, s, lo + n * warp / kJoinWarps, lo + n * (warp + 1) / kJoinWarps, c);
 #pragma unroll
-                for (int i = 1; i < kJoinWarps; ++i) add4(s, s_part[i][lane]);
-                write_row<kDeBf16, 4>(a, s_id[w], cq, reinterpret_cast<const float *>(&s), old);
-            }
-            __syncthreads();
+        for (int q = 0; q < kJoinRuns; ++q) s_part[warp][q][lane] = s[q];
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int i = 1; i < kJoinWarps; ++i)
+#pragma unroll
+                for (int q = 0; q < kJoinRuns; ++q) add4(s[q], s_part[i][q][lane]);
+            finish(s_id[w], s);
         }
+        __syncthreads();
     }
 }
 

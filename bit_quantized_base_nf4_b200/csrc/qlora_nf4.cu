@@ -987,7 +987,7 @@ static qlora_status check_ids(const void *ids, int ids_bytes, int64_t T, int64_t
 
 }  // extern "C" (a template has no C linkage)
 
-template <int kTable>
+template <int kTable, bool kDq>
 static qlora_status launch_embed_fwd(emb::FwdArgs &a, const void *ids, int ids_bytes, int64_t T, int64_t V, int64_t H,
                                      float scale, void *Y, int y_is_bf16, void *stream) {
     QL_TRY(check_ids(ids, ids_bytes, T, V, H));
@@ -999,18 +999,20 @@ static qlora_status launch_embed_fwd(emb::FwdArgs &a, const void *ids, int ids_b
     const int64_t segs = ceil_div(H, emb::kRun);
     a.seg_shift = 0;
     while ((1 << a.seg_shift) < segs && (2 << a.seg_shift) <= emb::kFwdWarps) ++a.seg_shift;
-    const int64_t gx = ceil_div(T, emb::kFwdWarps >> a.seg_shift), gy = ceil_div(segs, int64_t(1) << a.seg_shift);
+    const int64_t gy = ceil_div(segs, int64_t(1) << a.seg_shift), per_pass = emb::kFwdWarps >> a.seg_shift;
     if (gy > 65535) return fail(QLORA_ERR_SHAPE, "the row length (%lld) is too large", (long long)H);
     QL_TRY(require_sm100());
+    // several tokens a warp once the batch fills the device (8 CTAs per SM) four times over
+    a.passes = ceil_div(T, per_pass) * gy >= int64_t(sm_count()) * 8 * emb::kFwdPasses ? emb::kFwdPasses : 1;
     a.ids = emb::Ids{ids, ids_bytes == 8};
     a.out = Y;
     a.T = T;
     a.V = V;
-    a.H = H;
+    a.H = static_cast<int>(H);
     a.scale = scale;
     return launch_pdl("embed_fwd_kernel launch",
-                      y_is_bf16 ? emb::embed_fwd_kernel<kTable, true> : emb::embed_fwd_kernel<kTable, false>,
-                      dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), emb::kFwdThreads, 0,
+                      y_is_bf16 ? emb::embed_fwd_kernel<kTable, kDq, true> : emb::embed_fwd_kernel<kTable, kDq, false>,
+                      dim3(static_cast<unsigned>(ceil_div(T, per_pass * a.passes)), static_cast<unsigned>(gy)), emb::kFwdThreads, 0,
                       static_cast<cudaStream_t>(stream), a);
 }
 
@@ -1024,7 +1026,9 @@ qlora_status qlora_embed_nf4_fwd(const qlora_nf4_weight *w, const void *ids, int
     a.sc = scale_src(w);
     const Codebook &cb = codebook_for(w->quant_type);
     for (int i = 0; i < 16; ++i) a.level[i] = cb.level[i];
-    return launch_embed_fwd<emb::kTableNf4>(a, ids, ids_bytes, T, w->n_out, w->n_in, scale, Y, y_is_bf16, stream);
+    if (fmt_dq(w->format))
+        return launch_embed_fwd<emb::kTableNf4, true>(a, ids, ids_bytes, T, w->n_out, w->n_in, scale, Y, y_is_bf16, stream);
+    return launch_embed_fwd<emb::kTableNf4, false>(a, ids, ids_bytes, T, w->n_out, w->n_in, scale, Y, y_is_bf16, stream);
 }
 
 qlora_status qlora_embed_q8_0_fwd(const qlora_q8_0_weight *w, const void *ids, int ids_bytes, int64_t T, float scale,
@@ -1033,7 +1037,7 @@ qlora_status qlora_embed_q8_0_fwd(const qlora_q8_0_weight *w, const void *ids, i
     emb::FwdArgs a = {};
     a.table = w->q;
     a.d8 = w->d;
-    return launch_embed_fwd<emb::kTableQ8>(a, ids, ids_bytes, T, w->n_out, w->n_in, scale, Y, y_is_bf16, stream);
+    return launch_embed_fwd<emb::kTableQ8, false>(a, ids, ids_bytes, T, w->n_out, w->n_in, scale, Y, y_is_bf16, stream);
 }
 
 qlora_status qlora_embed_fwd(const void *E, int e_is_bf16, int64_t V, int64_t H, const void *ids, int ids_bytes,
@@ -1043,8 +1047,8 @@ qlora_status qlora_embed_fwd(const void *E, int e_is_bf16, int64_t V, int64_t H,
     if (e_is_bf16 != 0 && e_is_bf16 != 1) return fail(QLORA_ERR_ARG, "e_is_bf16 must be 0 or 1");
     emb::FwdArgs a = {};
     a.table = E;
-    if (e_is_bf16) return launch_embed_fwd<emb::kTableBf16>(a, ids, ids_bytes, T, V, H, scale, Y, y_is_bf16, stream);
-    return launch_embed_fwd<emb::kTableF32>(a, ids, ids_bytes, T, V, H, scale, Y, y_is_bf16, stream);
+    if (e_is_bf16) return launch_embed_fwd<emb::kTableBf16, false>(a, ids, ids_bytes, T, V, H, scale, Y, y_is_bf16, stream);
+    return launch_embed_fwd<emb::kTableF32, false>(a, ids, ids_bytes, T, V, H, scale, Y, y_is_bf16, stream);
 }
 
 // Sorted tokens per chunk of the gradient's reduction: a power of two in [8, 64], about eight blocks per
@@ -1105,9 +1109,17 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
     QL_TRY(require_sm100());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T > 0) {
-        QL_TRY(set_smem(emb::embed_sort_kernel, emb::kSortSmem));
-        QL_TRY(launch_pdl("embed_sort_kernel launch", emb::embed_sort_kernel, dim3(emb::kSortCtas), emb::kSortThreads,
-                          emb::kSortSmem, st, a));
+        if (T <= emb::kOneTokens) {
+            void (*const sort)(emb::GradArgs) = T <= emb::kSortThreads        ? emb::embed_sort_kernel<1>
+                                                : T <= 4 * emb::kSortThreads ? emb::embed_sort_kernel<4>
+                                                                             : emb::embed_sort_kernel<emb::kOneRounds>;
+            QL_TRY(set_smem(sort, emb::one_smem(T)));
+            QL_TRY(launch_pdl("embed_sort_kernel launch", sort, dim3(1), emb::kSortThreads, emb::one_smem(T), st, a));
+        } else {
+            QL_TRY(set_smem(emb::embed_sort_cluster_kernel, emb::kSortSmem));
+            QL_TRY(launch_pdl("embed_sort_cluster_kernel launch", emb::embed_sort_cluster_kernel, dim3(emb::kSortCtas),
+                              emb::kSortThreads, emb::kSortSmem, st, a));
+        }
         void (*const reduce[8])(emb::GradArgs) = {
             emb::embed_reduce_kernel<false, false, false>, emb::embed_reduce_kernel<false, false, true>,
             emb::embed_reduce_kernel<false, true, false>,  emb::embed_reduce_kernel<false, true, true>,
