@@ -266,7 +266,7 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t *p, uint32_t rank)
     return v;
 }
 
-// The first sweep's ranking: the place of a token among the equal digits that its warp has met so far.
+// The place of a token among the equal digits that its warp has met so far, counted in my[].
 __device__ __forceinline__ uint32_t rank_digit(uint32_t *my, uint32_t d, bool in, int lane) {
     const uint32_t same = __match_any_sync(0xffffffffu, in ? d : uint32_t(kMaxBins));   // idle lanes match none
     const uint32_t lower = same & ((1u << lane) - 1u);
@@ -304,70 +304,110 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t n, uint32_t *wsum, int
     return base + incl - n;
 }
 
-// One CTA sorts up to 1024 kRounds tokens: keys and places in registers, exchanged through shared memory.
-// Tokens are dealt in order to warps and rounds of 32, so a token's place among equal digits is the count in
-// lower warps, in its warp's earlier rounds and in its lower lanes: stable without atomics.
-constexpr int kOneRounds = 16;
-constexpr int kOneTokens = kOneRounds * kSortThreads;
-constexpr int one_smem(int64_t T) { return kSortSmem + 8 * kSortThreads * int((T + kSortThreads - 1) / kSortThreads); }
-template <int kRounds>
-__device__ void sort_one(const GradArgs &a, uint32_t *smem) {
-    uint32_t *hist = smem, *first = hist + kSortWarps * kMaxBins, *wsum = first + 2 * kMaxBins;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = static_cast<int>(a.T);
-    const int rounds = (T + kSortThreads - 1) / kSortThreads;         // at most kRounds
-    uint32_t *keys = smem + kSortSmem / 4, *places = keys + rounds * kSortThreads;
-    const int i0 = warp * rounds * 32 + lane, bins = 1 << a.bits;
+// Radix sort, least significant digit first, by one CTA (up to 4096 tokens) or by the cluster of kSortCtas (up to
+// 131072), with a CTA's tokens in registers.  Tokens are dealt in order to CTAs, warps and rounds of 32, so a
+// token's place among equal digits is the count in lower CTAs, in lower warps, in its warp's earlier rounds and
+// in its lower lanes: stable without atomics.  A CTA reorders its tokens in shared memory first, so that what it
+// writes to global memory comes in runs (scattered 4-byte stores kept one SM busy for 25 us per 16384 tokens).
+constexpr int kCtaRounds = 16;                       // most rounds of 1024 tokens a CTA holds
+constexpr int kOneTokens = 4 * kSortThreads;
+constexpr int kHeldTokens = kCtaRounds * kSortThreads * kSortCtas;
+constexpr int kHeldWords = kSortWarps * kMaxBins + 4 * kMaxBins + 64;
+constexpr int held_smem(int rounds) { return 4 * kHeldWords + 8 * kSortThreads * rounds; }
+template <bool kCluster, int kRounds>
+__device__ void sort_held(const GradArgs &a, uint32_t *smem, int rounds) {
+    uint32_t *hist = smem;                           // [warp][bin]
+    uint32_t *total = hist + kSortWarps * kMaxBins;  // [bin] of this CTA
+    uint32_t *local = total + kMaxBins;              // [bin] first place of the bin among this CTA's tokens
+    uint32_t *delta = local + kMaxBins;              // [bin] from there to its first place in the whole list
+    uint32_t *wsum = delta + kMaxBins;               // [warp] sums of a scan, twice
+    uint32_t *keys = smem + kHeldWords, *places = keys + rounds * kSortThreads;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, bins = 1 << a.bits;
+    const uint32_t rank = kCluster ? cluster_rank() : 0u;
+    const int64_t lo = min(int64_t(rank) * rounds * kSortThreads, a.T);
+    const int n = static_cast<int>(min(int64_t(rounds) * kSortThreads, a.T - lo));    // this CTA's tokens
+    const int i0 = warp * rounds * 32 + lane;
     uint32_t *my = hist + warp * kMaxBins;
     uint32_t k[kRounds], p[kRounds], r[kRounds];
 #pragma unroll
     for (int u = 0; u < kRounds; ++u) {
+        if (u >= rounds) break;
         const int t = i0 + 32 * u;
-        k[u] = u < rounds && t < T ? key_of(a, t) : 0u;
-        p[u] = t;
+        k[u] = t < n ? key_of(a, lo + t) : 0u;
+        p[u] = static_cast<uint32_t>(lo + t);
     }
     if (!a.accumulate) {
 #pragma unroll
-        for (int u = 0; u < kRounds; ++u)
-            if (u < rounds && i0 + 32 * u < T && k[u] < a.V) atomicOr(a.named + (k[u] >> 5), 1u << (k[u] & 31));
+        for (int u = 0; u < kRounds; ++u) {
+            if (u >= rounds) break;
+            if (i0 + 32 * u < n && k[u] < a.V) atomicOr(a.named + (k[u] >> 5), 1u << (k[u] & 31));
+        }
     }
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = pass * a.bits;
         for (int b = lane; b < bins; b += 32) my[b] = 0;
         __syncwarp();
 #pragma unroll
-        for (int u = 0; u < kRounds; ++u)
-            if (u < rounds) r[u] = rank_digit(my, (k[u] >> shift) & (bins - 1), i0 + 32 * u < T, lane);
-        __syncthreads();
-        const uint32_t total = tid < bins ? scan_warps(hist, tid) : 0u;
-        const uint32_t base = scan_threads(total, wsum, warp, lane);
-        if (tid < bins) first[tid] = base;
-        __syncthreads();
-        const bool last = pass + 1 == a.passes;
-#pragma unroll
         for (int u = 0; u < kRounds; ++u) {
-            if (u >= rounds || i0 + 32 * u >= T) continue;
-            const uint32_t d = (k[u] >> shift) & (bins - 1), at = first[d] + my[d] + r[u];
-            if (last) {
-                __stcg(a.key[a.passes & 1] + at, k[u]);
-                __stcg(a.pos[a.passes & 1] + at, p[u]);
-            } else {
-                keys[at] = k[u];
-                places[at] = p[u];
+            if (u >= rounds) break;
+            r[u] = rank_digit(my, (k[u] >> shift) & (bins - 1), i0 + 32 * u < n, lane);
+        }
+        __syncthreads();
+        const uint32_t mine = tid < bins ? scan_warps(hist, tid) : 0u;
+        uint32_t below = 0, all = mine;
+        if (kCluster) {
+            if (tid < bins) total[tid] = mine;
+            cluster_barrier();
+            all = 0;
+            if (tid < bins) {
+#pragma unroll
+                for (uint32_t c = 0; c < kSortCtas; ++c) {
+                    const uint32_t x = ld_cluster(total + tid, c);
+                    all += x;
+                    if (c < rank) below += x;
+                }
             }
         }
-        if (last) return;
+        const uint32_t in_cta = scan_threads(mine, wsum, warp, lane);
+        const uint32_t in_list = kCluster ? scan_threads(all, wsum + kSortWarps, warp, lane) + below : in_cta;
+        if (tid < bins) {
+            local[tid] = in_cta;
+            delta[tid] = in_list - in_cta;
+        }
         __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) {
+            if (u >= rounds || i0 + 32 * u >= n) break;          // a lane's places ascend
+            const uint32_t d = (k[u] >> shift) & (bins - 1), at = local[d] + my[d] + r[u];
+            keys[at] = k[u];
+            places[at] = p[u];
+        }
+        __syncthreads();
+        const bool last = pass + 1 == a.passes;
+        if (kCluster || last) {
+            uint32_t *dst_k = a.key[(pass + 1) & 1], *dst_p = a.pos[(pass + 1) & 1];
+            for (int j = tid; j < n; j += kSortThreads) {
+                const uint32_t key = keys[j], at = j + delta[(key >> shift) & (bins - 1)];
+                __stcg(dst_k + at, key);
+                __stcg(dst_p + at, places[j]);
+            }
+            if (last) break;
+            cluster_barrier();   // the next pass reads what every CTA wrote; total is free again
+        }
 #pragma unroll
         for (int u = 0; u < kRounds; ++u) {
             const int t = i0 + 32 * u;
-            if (u < rounds && t < T) k[u] = keys[t], p[u] = places[t];
+            if (u >= rounds || t >= n) break;
+            k[u] = kCluster ? __ldcg(a.key[(pass + 1) & 1] + lo + t) : keys[t];
+            p[u] = kCluster ? __ldcg(a.pos[(pass + 1) & 1] + lo + t) : places[t];
         }
     }
+    if (kCluster) cluster_barrier();   // no CTA leaves while another may read its totals
 }
 
-// More tokens: the cluster of kSortCtas CTAs sorts with the same dealing over CTAs, warps and rounds; bins and
-// counts meet in shared memory of the cluster, tokens in global memory (L2), one digit after the other.
-__device__ void sort_cluster(const GradArgs &a, uint32_t *smem) {
+// More tokens than the cluster holds: the same dealing, with two sweeps over the tokens in global memory per
+// digit, to count and to place them.
+__device__ void sort_swept(const GradArgs &a, uint32_t *smem) {
     uint32_t *hist = smem;                               // [warp][bin]
     uint32_t *total = hist + kSortWarps * kMaxBins;      // [bin] of this CTA
     uint32_t *first = total + kMaxBins;                  // [bin] first place of this CTA's tokens
@@ -434,27 +474,37 @@ __device__ void sort_cluster(const GradArgs &a, uint32_t *smem) {
     }
 }
 
-__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort_cluster_kernel(const GradArgs a) {
-    extern __shared__ uint32_t sort_smem[];
-    pdl_launch_dependents();
-    pdl_wait();
-    if (!a.accumulate) {        // no row is named yet; the sort's first pass marks them
-        for (int64_t i = int64_t(cluster_rank()) * kSortThreads + threadIdx.x; i < (a.V + 31) / 32; i += kSortCtas * kSortThreads)
-            __stcg(a.named + i, 0u);
-        cluster_barrier();
-    }
-    sort_cluster(a, sort_smem);
+// no row is named yet; the sort's first pass marks the rows
+template <bool kCluster>
+__device__ __forceinline__ void clear_named(const GradArgs &a) {
+    if (a.accumulate) return;
+    const int64_t first = (kCluster ? int64_t(cluster_rank()) * kSortThreads : 0) + threadIdx.x;
+    for (int64_t i = first; i < (a.V + 31) / 32; i += (kCluster ? kSortCtas : 1) * kSortThreads) __stcg(a.named + i, 0u);
+    if (kCluster) cluster_barrier();
+    else __syncthreads();
 }
 template <int kRounds>
-__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kSortThreads) embed_sort_one_kernel(const GradArgs a, int rounds) {
     extern __shared__ uint32_t sort_smem[];
     pdl_launch_dependents();
     pdl_wait();
-    if (!a.accumulate) {
-        for (int64_t i = threadIdx.x; i < (a.V + 31) / 32; i += kSortThreads) __stcg(a.named + i, 0u);
-        __syncthreads();
-    }
-    sort_one<kRounds>(a, sort_smem);
+    clear_named<false>(a);
+    sort_held<false, kRounds>(a, sort_smem, rounds);
+}
+template <int kRounds>
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort_held_kernel(const GradArgs a, int rounds) {
+    extern __shared__ uint32_t sort_smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    clear_named<true>(a);
+    sort_held<true, kRounds>(a, sort_smem, rounds);
+}
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort_swept_kernel(const GradArgs a) {
+    extern __shared__ uint32_t sort_smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    clear_named<true>(a);
+    sort_swept(a, sort_smem);
 }
 
 // Zero: a CTA of 256 threads for about 16 KB of rows, in the order of the table.  (A grid of two CTAs per SM

@@ -1109,15 +1109,19 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
     QL_TRY(require_sm100());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T > 0) {
-        if (T <= emb::kOneTokens) {
-            void (*const sort)(emb::GradArgs) = T <= emb::kSortThreads        ? emb::embed_sort_kernel<1>
-                                                : T <= 4 * emb::kSortThreads ? emb::embed_sort_kernel<4>
-                                                                             : emb::embed_sort_kernel<emb::kOneRounds>;
-            QL_TRY(set_smem(sort, emb::one_smem(T)));
-            QL_TRY(launch_pdl("embed_sort_kernel launch", sort, dim3(1), emb::kSortThreads, emb::one_smem(T), st, a));
+        if (T <= emb::kHeldTokens) {
+            const bool one = T <= emb::kOneTokens;
+            const int rounds = static_cast<int>(ceil_div(T, int64_t(one ? 1 : emb::kSortCtas) * emb::kSortThreads));
+            void (*sort)(emb::GradArgs, int);
+            if (one) sort = rounds == 1 ? emb::embed_sort_one_kernel<1> : emb::embed_sort_one_kernel<4>;
+            else if (rounds <= 2) sort = emb::embed_sort_held_kernel<2>;
+            else sort = rounds <= 4 ? emb::embed_sort_held_kernel<4> : emb::embed_sort_held_kernel<emb::kCtaRounds>;
+            QL_TRY(set_smem(sort, emb::held_smem(rounds)));
+            QL_TRY(launch_pdl("embed_sort kernel launch", sort, dim3(one ? 1 : emb::kSortCtas), emb::kSortThreads,
+                              emb::held_smem(rounds), st, a, rounds));
         } else {
-            QL_TRY(set_smem(emb::embed_sort_cluster_kernel, emb::kSortSmem));
-            QL_TRY(launch_pdl("embed_sort_cluster_kernel launch", emb::embed_sort_cluster_kernel, dim3(emb::kSortCtas),
+            QL_TRY(set_smem(emb::embed_sort_swept_kernel, emb::kSortSmem));
+            QL_TRY(launch_pdl("embed_sort_swept_kernel launch", emb::embed_sort_swept_kernel, dim3(emb::kSortCtas),
                               emb::kSortThreads, emb::kSortSmem, st, a));
         }
         void (*const reduce[8])(emb::GradArgs) = {

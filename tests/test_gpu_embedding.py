@@ -162,6 +162,9 @@ GRAD = [
     (9001, 300_000, 40, "any", torch.bfloat16, torch.bfloat16, False, 7, 1.0, torch.int64),
     (30_000, 100, 3000 // 8 * 8, "zipf", torch.bfloat16, torch.float32, True, 3, 1.0, torch.int64),
     (70_001, 262_144, 16, "zipf", torch.float32, torch.float32, False, -1, 1.0, torch.int32),
+    (131_072, 50_000, 8, "zipf", torch.float32, torch.float32, False, -1, 1.0, torch.int64),
+    (131_073, 50_000, 8, "zipf", torch.float32, torch.float32, False, -1, 1.0, torch.int64),
+    (200_003, 300_000, 24, "any", torch.bfloat16, torch.float32, True, 5, 1.0, torch.int32),
 ]
 
 
