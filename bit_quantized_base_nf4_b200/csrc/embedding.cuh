@@ -355,7 +355,7 @@ __device__ void sort_held(const GradArgs &a, uint32_t *smem, int rounds) {
         __syncthreads();
         const uint32_t mine = tid < bins ? scan_warps(hist, tid) : 0u;
         uint32_t below = 0, all = mine;
-        if (kCluster) {
+        if constexpr (kCluster) {
             if (tid < bins) total[tid] = mine;
             cluster_barrier();
             all = 0;
@@ -589,7 +589,7 @@ __device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64
 // kBatch rows of dY in flight, with the old rows of dE that they will be added to.
 constexpr int kRedThreads = 128;
 constexpr int kRedCols = kRedThreads * 8;
-constexpr int kMaxChunk = 64;
+constexpr int kMaxChunk = 128;
 constexpr int kBatch = 4;
 template <bool kDyBf16, bool kDeBf16, bool kAdd>
 __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArgs a) {

@@ -207,13 +207,15 @@ __device__ __forceinline__ void block_step(float a, float top2, float &d, float 
 // Codes of a lane's 8 values given inv = RN(1 / d).  kSecond = false: x holds m.  Otherwise x holds v, of
 // which y = RN(RN(sqrt(v)) inv) is coded, and w its approximate root.  The candidate is the
 // nearest integer to an approximate sqrt(y - 1/4): relative errors of 2^-23 for w and for the root and 2^-24 for
-// the product put it within 255 * 1.75 * 2^-23 = 5.4e-5.  Only where that root lies within 1e-4 of a half is y formed
-// exactly and the candidate checked against the borders.
+// the product put it within 255 * 1.75 * 2^-23 = 5.4e-5 (m: 127 * 1.25 * 2^-23 = 1.9e-5).  Only where that root lies
+// closer to a half is y formed exactly and the candidate checked against the borders: in 3 % (m: 1 %) of
+// the blocks, for the elements concerned.
 constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer in the low mantissa bits
 template <bool kSecond>
 __device__ __forceinline__ void encode8(const float *x, const float *w, float inv, bool exact, uint32_t *c) {
+    constexpr float kNear = kSecond ? 0.49994f : 0.499975f;
     uint32_t t[8];
-    float off = exact ? 1.f : 0.f;
+    float e[8], off = exact ? 1.f : 0.f;
     const uint64_t magic = pack2(kMagic, kMagic), minus = pack2(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -231,28 +233,23 @@ __device__ __forceinline__ void encode8(const float *x, const float *w, float in
             z1 = copysignf(z1, x[i + 1]);
         }
         const uint64_t z = pack2(z0, z1), r = add2(z, magic);
-        float e0, e1, r0, r1;
-        unpack2(add2(z, fma2(r, minus, magic)), e0, e1);    // z - (r - magic)
-        off = fmaxf(off, fmaxf(fabsf(e0), fabsf(e1)));
+        float r0, r1;
+        unpack2(add2(z, fma2(r, minus, magic)), e[i], e[i + 1]);    // z - (r - magic)
+        off = fmaxf(off, fmaxf(fabsf(e[i]), fabsf(e[i + 1])));
         unpack2(r, r0, r1);
         t[i] = __float_as_uint(r0);
         t[i + 1] = __float_as_uint(r1);
     }
-    if (off > 0.4999f) {
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            // places of x, w and t are picked without dynamic indexing
-            float xi = x[0];
+    if (__any_sync(0xffffffffu, off > kNear)) {
 #pragma unroll
-            for (int j = 1; j < 8; ++j) xi = i == j ? x[j] : xi;
-            const float y = __fmul_rn(kSecond ? __fsqrt_rn(xi) : fabsf(xi), inv);
+        for (int i = 0; i < 8; ++i) {
+            if (!__any_sync(0xffffffffu, exact || fabsf(e[i]) > kNear)) continue;
+            const float y = __fmul_rn(kSecond ? __fsqrt_rn(x[i]) : fabsf(x[i]), inv);
             float k = rintf(sqrt_approx<true>(fmaxf(__fsub_rn(y, 0.25f), 0.f)));
             // k^2 + k + 1/2 is exact: at most 17 significant bits
             if (y > __fmaf_rn(k, k, k) + 0.5f) k += 1.f;
             else if (k > 0.f && y <= __fmaf_rn(k, k, -k) + 0.5f) k -= 1.f;
-            const uint32_t b = __float_as_uint(__fadd_rn(kSecond ? k : copysignf(k, xi), kMagic));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) t[j] = i == j ? b : t[j];
+            t[i] = __float_as_uint(__fadd_rn(kSecond ? k : copysignf(k, x[i]), kMagic));
         }
     }
 #pragma unroll
@@ -266,9 +263,10 @@ struct StepArgs {
     const float *coef;         // clip coefficient on the device, or NULL
     const float *lr_dev;       // learning rate on the device, or NULL
     int counted;               // 1: ds and de are in the head (step_scalars_kernel)
-    int64_t nchunks;
-    float lr, b1, w1, b2, w2;  // w = 1 - b
-    float one;                 // 1, as a value that the compiler does not know
+    int nchunks;
+    uint64_t b1, w1, b2, w2;   // pairs of b and w = 1 - b
+    uint64_t one;              // a pair of 1, as a value that the compiler does not know
+    float lr;
     float ds, de;              // (1 - b1^t) / sqrt(1 - b2^t) and (1 - b1^t) eps
 };
 
@@ -353,10 +351,9 @@ struct Raw8 {
 // rounded one by one: the sum is a product with the argument `one`, because a plain paired product and
 // sum were merged into one rounding by the assembler (codes then differed).
 __device__ __forceinline__ void moments(const StepArgs &a, const Scalars &s, uint64_t g, uint64_t &m, uint64_t &v) {
-    const uint64_t one = pack2(a.one, a.one);
     g = mul2(g, pack2(s.coef, s.coef));
-    m = fma2(mul2(pack2(a.b1, a.b1), m), one, mul2(pack2(a.w1, a.w1), g));
-    v = fma2(mul2(pack2(a.b2, a.b2), v), one, mul2(pack2(a.w2, a.w2), mul2(g, g)));
+    m = fma2(mul2(a.b1, m), a.one, mul2(a.w1, g));
+    v = fma2(mul2(a.b2, v), a.one, mul2(a.w2, mul2(g, g)));
 }
 // the approximate roots w of a lane's 8 second moments
 __device__ __forceinline__ void roots(const Scalars &s, const float *v, float *w) {
@@ -368,11 +365,12 @@ __device__ __forceinline__ void roots(const Scalars &s, const float *v, float *w
         for (int i = 0; i < 8; ++i) w[i] = sqrt_approx<false>(v[i]);
     }
 }
-__device__ __forceinline__ uint64_t update(const Scalars &s, float lr, float decay, uint64_t p, uint64_t m, float w0, float w1) {
+// minus_lr, decay: pairs
+__device__ __forceinline__ uint64_t update(const Scalars &s, uint64_t minus_lr, uint64_t decay, uint64_t p, uint64_t m, float w0, float w1) {
     float d0, d1;
     unpack2(fma2(pack2(w0, w1), pack2(s.ds, s.ds), pack2(s.de, s.de)), d0, d1);
     const uint64_t u = mul2(m, pack2(rcp_approx(d0), rcp_approx(d1)));
-    return fma2(pack2(-lr, -lr), fma2(pack2(decay, decay), p, u), p);
+    return fma2(minus_lr, fma2(decay, p, u), p);
 }
 
 // ---- 32-bit states: 30 bytes per fp32 parameter, bound by HBM.
@@ -396,9 +394,10 @@ __device__ __forceinline__ void step32_block(const StepArgs &a, const Scalars &s
         unpack2(vp, vf[2 * i], vf[2 * i + 1]);
     }
     roots(s, vf, w);
+    const float lr = -(s.lr * c.lr_scale);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        unpack2(update(s, s.lr * c.lr_scale, c.decay, p.pair(i), mp[i], w[2 * i], w[2 * i + 1]), pf[2 * i], pf[2 * i + 1]);
+        unpack2(update(s, pack2(lr, lr), pack2(c.decay, c.decay), p.pair(i), mp[i], w[2 * i], w[2 * i + 1]), pf[2 * i], pf[2 * i + 1]);
     store8<kFull>(c.p, kPBf16, i0, rem, lane, pf);
     if (!kPBf16 && c.copy) store8<kFull>(c.copy, true, i0, rem, lane, pf);
     store8<kFull>(c.m, false, i0, rem, lane, mf);
@@ -415,7 +414,7 @@ __device__ __forceinline__ void step32_chunk(const StepArgs &a, const Scalars &s
 // where this takes 583, on 129 M fp32 parameters with bf16 copies).
 __global__ void __launch_bounds__(kThreads, 4) adamw32_kernel(const StepArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t i = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
     // the chunk list was complete when the plan's call returned: it may be read before the wait
     const uint32_t word = i < a.nchunks ? chunk_word(a.chunks, i, lane) : 0u;
     pdl_launch_dependents();
@@ -442,49 +441,70 @@ __global__ void __launch_bounds__(kThreads, 4) adamw32_kernel(const StepArgs a) 
 constexpr int kStages = 3;
 constexpr int kStageBytes = kBlock * (4 + 4 + 1 + 1);      // g, p, m, v
 constexpr int kSlots = 4;                                  // chunks between the block worked on and the one copied
-constexpr int kStep8Smem = kWarps * (kStages * kStageBytes + kSlots * int(sizeof(Chunk)));
+// A chunk at hand, in the warp's shared memory: the list's 80 bytes, and its rate and decay as pairs.
+struct alignas(16) Slot {
+    Chunk c;
+    uint64_t minus_lr, decay;
+};
+constexpr int kStep8Smem = kWarps * (kStages * kStageBytes + kSlots * int(sizeof(Slot)));
 
 template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t dst, uint64_t src, int bytes) {
+__device__ __forceinline__ void copy_async(uint32_t dst, uint64_t src) {
+    if (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else if (kBytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void copy_async_part(uint32_t dst, uint64_t src, int bytes) {
     if (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
     else if (kBytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// a lane's two runs of four elements (kSize bytes each) of the block at i0
+// a lane's two runs of four elements (kSize bytes each) of the block at i0, of which rem elements are there
 template <int kSize>
 __device__ __forceinline__ void copy_runs(uint32_t dst, uint64_t base, int i0, int rem, int lane) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int e = h * 128 + lane * 4;
-        copy_async<4 * kSize>(dst + e * kSize, base + uint64_t(i0 + e) * kSize, kSize * min(max(rem - e, 0), 4));
+    const uint64_t src = base + static_cast<uint32_t>((i0 + lane * 4) * kSize);
+    dst += lane * 4 * kSize;
+    if (rem >= kBlock) {
+        copy_async<4 * kSize>(dst, src);
+        copy_async<4 * kSize>(dst + 128 * kSize, src + 128 * kSize);
+    } else {
+        rem -= lane * 4;
+        copy_async_part<4 * kSize>(dst, src, kSize * min(max(rem, 0), 4));
+        copy_async_part<4 * kSize>(dst + 128 * kSize, src + 128 * kSize, kSize * min(max(rem - 128, 0), 4));
     }
 }
 __device__ __forceinline__ void copy_block(const Chunk &c, uint32_t stage, int i0, int lane) {
     const int rem = c.n - i0;
-    if (c.flags & kGradBf16) copy_runs<2>(stage, c.g, i0, rem, lane);
+    const uint32_t flags = c.flags;
+    if (flags & kGradBf16) copy_runs<2>(stage, c.g, i0, rem, lane);
     else copy_runs<4>(stage, c.g, i0, rem, lane);
-    if (c.flags & kParamBf16) copy_runs<2>(stage + 4 * kBlock, c.p, i0, rem, lane);
+    if (flags & kParamBf16) copy_runs<2>(stage + 4 * kBlock, c.p, i0, rem, lane);
     else copy_runs<4>(stage + 4 * kBlock, c.p, i0, rem, lane);
     copy_runs<1>(stage + 8 * kBlock, c.m, i0, rem, lane);
     copy_runs<1>(stage + 9 * kBlock, c.v, i0, rem, lane);
 }
-// pair i (of 4) of a lane's elements of a parameter or gradient in a stage
+// pairs 2 h and 2 h + 1 of a lane's elements of a parameter or gradient in a stage
 template <bool kBf16>
-__device__ __forceinline__ uint64_t stage_pair(const uint8_t *base, int i, int lane) {
-    const int e = (i >> 1) * 128 + lane * 4 + 2 * (i & 1);
+__device__ __forceinline__ void stage_pairs(const uint8_t *base, int h, int lane, uint64_t *x) {
+    const int e = h * 128 + lane * 4;
     if (kBf16) {
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(base + 2 * e);
-        return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        const uint2 w = *reinterpret_cast<const uint2 *>(base + 2 * e);
+        x[0] = pack2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u));
+        x[1] = pack2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+    } else {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(base + 4 * e);
+        x[0] = w.x;
+        x[1] = w.y;
     }
-    return *reinterpret_cast<const uint64_t *>(base + 4 * e);
 }
 
 template <bool kPBf16, bool kGBf16, bool kFull>
-__device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s, const Chunk &c, const uint8_t *stage, float dm,
+__device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s, const Slot &c, const uint8_t *stage, float dm,
                                             float dv, int i0, int lane) {
-    const int rem = c.n - i0;
+    const int rem = c.c.n - i0;
     float mf[8], vf[8], w[8], pf[8];
-    uint64_t m[4], v[4];
+    uint64_t m[4], v[4], x[2];
     uint32_t cm[2], cv[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -495,17 +515,20 @@ __device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s,
     decode8<true>(cv, dv, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        moments(a, s, stage_pair<kGBf16>(stage, i, lane), m[i], v[i]);
+        if (i % 2 == 0) stage_pairs<kGBf16>(stage, i / 2, lane, x);
+        moments(a, s, x[i % 2], m[i], v[i]);
         unpack2(m[i], mf[2 * i], mf[2 * i + 1]);
         unpack2(v[i], vf[2 * i], vf[2 * i + 1]);
     }
     roots(s, vf, w);
+    const uint64_t minus_lr = c.minus_lr, decay = c.decay;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        unpack2(update(s, s.lr * c.lr_scale, c.decay, stage_pair<kPBf16>(stage + 4 * kBlock, i, lane), m[i], w[2 * i], w[2 * i + 1]),
-                pf[2 * i], pf[2 * i + 1]);
-    store8<kFull>(c.p, kPBf16, i0, rem, lane, pf);
-    if (!kPBf16 && c.copy) store8<kFull>(c.copy, true, i0, rem, lane, pf);
+    for (int i = 0; i < 4; ++i) {
+        if (i % 2 == 0) stage_pairs<kPBf16>(stage + 4 * kBlock, i / 2, lane, x);
+        unpack2(update(s, minus_lr, decay, x[i % 2], m[i], w[2 * i], w[2 * i + 1]), pf[2 * i], pf[2 * i + 1]);
+    }
+    store8<kFull>(c.c.p, kPBf16, i0, rem, lane, pf);
+    if (!kPBf16 && c.c.copy) store8<kFull>(c.c.copy, true, i0, rem, lane, pf);
     float am = 0.f, av = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -524,55 +547,61 @@ __device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s,
     encode8<false>(mf, nullptr, __shfl_sync(0xffffffffu, inv, 0), false, cm);
     // below 2^-92 a flushed root could have had a code above 0
     encode8<true>(vf, w, __shfl_sync(0xffffffffu, inv, 1), s.flush && av < 2.0194839e-28f, cv);
-    store_codes<kFull>(c.m, i0, rem, lane, cm);
-    store_codes<kFull>(c.v, i0, rem, lane, cv);
-    if (lane < 2) reinterpret_cast<float *>(lane ? c.dv : c.dm)[i0 / kBlock] = d;
+    store_codes<kFull>(c.c.m, i0, rem, lane, cm);
+    store_codes<kFull>(c.c.v, i0, rem, lane, cv);
+    if (lane < 2) reinterpret_cast<float *>(lane ? c.c.dv : c.c.dm)[i0 / kBlock] = d;
 }
 template <bool kPBf16, bool kGBf16>
-__device__ __forceinline__ void step8_any(const StepArgs &a, const Scalars &s, const Chunk &c, const uint8_t *stage, float dm,
+__device__ __forceinline__ void step8_any(const StepArgs &a, const Scalars &s, const Slot &c, const uint8_t *stage, float dm,
                                           float dv, int i0, int lane) {
-    if (c.n - i0 >= kBlock) step8_block<kPBf16, kGBf16, true>(a, s, c, stage, dm, dv, i0, lane);
+    if (c.c.n - i0 >= kBlock) step8_block<kPBf16, kGBf16, true>(a, s, c, stage, dm, dv, i0, lane);
     else step8_block<kPBf16, kGBf16, false>(a, s, c, stage, dm, dv, i0, lane);
 }
 
 constexpr int kCtas8 = 3;      // CTAs per SM that the registers are capped for
-__global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const StepArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const __grid_constant__ StepArgs a) {
     extern __shared__ __align__(16) uint8_t step8_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint8_t *ring = step8_smem + warp * (kStages * kStageBytes);
-    Chunk *slots = reinterpret_cast<Chunk *>(step8_smem + kWarps * kStages * kStageBytes) + warp * kSlots;
+    Slot *slots = reinterpret_cast<Slot *>(step8_smem + kWarps * kStages * kStageBytes) + warp * kSlots;
     const uint32_t ring_at = smem_u32(ring);
-    const int64_t stride = int64_t(gridDim.x) * kWarps;
-    int64_t done = int64_t(blockIdx.x) * kWarps + warp;       // the chunk worked on
+    const int stride = gridDim.x * kWarps;
+    int done = blockIdx.x * kWarps + warp;                    // the chunk worked on
     if (done >= a.nchunks) return;
     // the chunk list was complete when the plan's call returned: it may be read before the wait
-    int64_t ahead = done;                                     // the chunk copied from
-    if (lane < 20) reinterpret_cast<uint32_t *>(slots)[lane] = chunk_word(a.chunks, ahead, lane);
-    uint32_t word = ahead + stride < a.nchunks ? chunk_word(a.chunks, ahead + stride, lane) : 0u;
-    __syncwarp();
+    int ahead = done;                                         // the chunk copied from
+    uint32_t word = chunk_word(a.chunks, ahead, lane);
     pdl_launch_dependents();
     pdl_wait();
     Scalars s;
     if (!read_scalars(a, s)) return;
     int to_slot = 0, to_i0 = 0, to_stage = 0;
+    // the chunk `ahead`, whose words are here, into slot to_slot; the words of the one after it are sent for
+    auto open_slot = [&]() {
+        const float lr = -(s.lr * __uint_as_float(word32(word, 16))), decay = __uint_as_float(word32(word, 17));
+        __syncwarp();
+        if (lane < 20) reinterpret_cast<uint32_t *>(slots + to_slot)[lane] = word;
+        if (lane == 20) slots[to_slot].minus_lr = pack2(lr, lr);
+        if (lane == 21) slots[to_slot].decay = pack2(decay, decay);
+        __syncwarp();
+        if (ahead + stride < a.nchunks) word = chunk_word(a.chunks, ahead + stride, lane);
+    };
+    open_slot();
     float next_dm = 0.f, next_dv = 0.f;
     // starts the copies of the next block of the list, if there is one; every call closes one group
     auto copy_next = [&]() {
         if (ahead < a.nchunks) {
-            const Chunk &c = slots[to_slot];
+            const Chunk &c = slots[to_slot].c;
             copy_block(c, ring_at + to_stage * kStageBytes, to_i0, lane);
             to_i0 += kBlock;
             if (to_i0 >= c.n) {
                 to_i0 = 0;
                 ahead += stride;
                 to_slot = (to_slot + 1) % kSlots;
-                __syncwarp();
-                if (lane < 20) reinterpret_cast<uint32_t *>(slots + to_slot)[lane] = word;
-                __syncwarp();
-                if (ahead + stride < a.nchunks) word = chunk_word(a.chunks, ahead + stride, lane);
+                open_slot();
             }
         }
-        to_stage = (to_stage + 1) % kStages;
+        to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     auto steps_of = [&](const Chunk &c, int i0) {
@@ -582,29 +611,29 @@ __global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const StepArgs
     copy_next();
     copy_next();
     int slot = 0, stage = 0, i0 = 0;
-    steps_of(slots[0], 0);
+    steps_of(slots[0].c, 0);
     while (true) {
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         copy_next();
-        const Chunk &c = slots[slot];
+        const Slot &c = slots[slot];
         const float dm = next_dm, dv = next_dv;
         // the block after this one
         int n_slot = slot, n_i0 = i0 + kBlock;
-        if (n_i0 >= c.n) {
+        if (n_i0 >= c.c.n) {
             n_i0 = 0;
             n_slot = (slot + 1) % kSlots;
             done += stride;
         }
-        if (done < a.nchunks) steps_of(slots[n_slot], n_i0);
+        if (done < a.nchunks) steps_of(slots[n_slot].c, n_i0);
         const uint8_t *at = ring + stage * kStageBytes;
-        switch (c.flags & (kParamBf16 | kGradBf16)) {
+        switch (c.c.flags & (kParamBf16 | kGradBf16)) {
             case 0: step8_any<false, false>(a, s, c, at, dm, dv, i0, lane); break;
             case kParamBf16: step8_any<true, false>(a, s, c, at, dm, dv, i0, lane); break;
             case kGradBf16: step8_any<false, true>(a, s, c, at, dm, dv, i0, lane); break;
             default: step8_any<true, true>(a, s, c, at, dm, dv, i0, lane);
         }
         if (done >= a.nchunks) return;
-        stage = (stage + 1) % kStages;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         slot = n_slot;
         i0 = n_i0;
     }

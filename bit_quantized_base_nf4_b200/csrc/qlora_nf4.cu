@@ -1210,6 +1210,7 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     int64_t numel = 0;
     QL_TRY(check_opt_tensors(tensors, count, &numel));
     const int64_t chunk = plan_chunk(numel), nchunks = plan_chunks(tensors, count, chunk);
+    if (nchunks > (1 << 30)) return fail(QLORA_ERR_SHAPE, "the tensors have too many elements for one plan");
     const size_t need = sizeof(optim::PlanHead) + size_t(nchunks) * sizeof(optim::Chunk);
     if (!buffer || bytes < need) return fail(QLORA_ERR_WORKSPACE, "the plan buffer holds %zu bytes, %zu needed", buffer ? bytes : size_t(0), need);
     if (reinterpret_cast<uintptr_t>(buffer) % 256) return fail(QLORA_ERR_ALIGN, "the plan buffer must be 256-byte aligned");
@@ -1296,11 +1297,17 @@ qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double be
     a.coef = grad_scale;
     a.lr_dev = lr_dev;
     a.lr = lr_dev ? 0.f : static_cast<float>(lr);
-    a.one = 1.f;
-    a.b1 = static_cast<float>(beta1);
-    a.w1 = static_cast<float>(1.0 - beta1);
-    a.b2 = static_cast<float>(beta2);
-    a.w2 = static_cast<float>(1.0 - beta2);
+    auto pair = [](double x) {
+        const float f = static_cast<float>(x);
+        uint32_t u;
+        std::memcpy(&u, &f, 4);
+        return uint64_t(u) << 32 | u;
+    };
+    a.one = pair(1.0);
+    a.b1 = pair(beta1);
+    a.w1 = pair(1.0 - beta1);
+    a.b2 = pair(beta2);
+    a.w2 = pair(1.0 - beta2);
     if (step_dev) {
         a.counted = 1;
         QL_TRY(launch_pdl("step_scalars_kernel launch", optim::step_scalars_kernel, dim3(1), 1, 0, st, plan_head(plan), step_dev,
@@ -1312,13 +1319,13 @@ qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double be
     }
     if (plan->chunks32 > 0) {
         a.chunks = plan_list(plan);
-        a.nchunks = plan->chunks32;
+        a.nchunks = static_cast<int>(plan->chunks32);
         QL_TRY(launch_pdl("adamw32_kernel launch", optim::adamw32_kernel,
                           dim3(static_cast<unsigned>(ceil_div(a.nchunks, optim::kWarps))), optim::kThreads, 0, st, a));
     }
     if (plan->chunks > plan->chunks32) {
         a.chunks = plan_list(plan) + plan->chunks32;
-        a.nchunks = plan->chunks - plan->chunks32;
+        a.nchunks = static_cast<int>(plan->chunks - plan->chunks32);
         QL_TRY(set_smem(optim::adamw8_kernel, optim::kStep8Smem));
         QL_TRY(launch_pdl("adamw8_kernel launch", optim::adamw8_kernel, plan_grid(a.nchunks, optim::kCtas8), optim::kThreads,
                           optim::kStep8Smem, st, a));
