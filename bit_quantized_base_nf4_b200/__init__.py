@@ -304,6 +304,10 @@ def qlora_q8_0_lora_linear_bwd_dx(weight: Q80Weight, dY, A, B, r: int, scaling: 
 
 # ----------------------------------------------------------------------------- embedding
 
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _on(t, dev: int, name: str) -> None:
     """The calls launch on the current device: a tensor has to be contiguous and live there."""
     if t.get_device() != dev or not t.is_contiguous():
@@ -328,7 +332,8 @@ def _is_bf16(t, shape, dev: int, name: str) -> int:
     """1 for a bfloat16 tensor of that shape on the device, 0 for a float32 one; else an error."""
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _on(t, dev, name)
+    if t.get_device() != dev or not t.is_contiguous():
+        _on(t, dev, name)
     if t.dtype is torch.bfloat16:
         return 1
     if t.dtype is torch.float32:
@@ -344,7 +349,7 @@ def qlora_embed_fwd(table: torch.Tensor, ids: torch.Tensor, scale: float, Y: tor
     V, H = table.shape
     T = ids.numel()
     idb, tb, yb = _ids_bytes(ids, dev), _is_bf16(table, (V, H), dev, "table"), _is_bf16(Y, (T, H), dev, "Y")
-    st = _lib().qlora_embed_fwd(table.data_ptr(), tb, V, H, ids.data_ptr(), idb, T, scale, Y.data_ptr(), yb, _stream(stream))
+    st = _lib().qlora_embed_fwd(table.data_ptr(), tb, V, H, ids.data_ptr(), idb, T, scale, Y.data_ptr(), yb, _raw_stream(stream, dev))
     if st:
         _capi.check("qlora_embed_fwd", st)
 
@@ -354,7 +359,7 @@ def _embed_packed(name, f, weight, codes, ids, scale, Y, stream):
     T = ids.numel()
     idb, yb = _ids_bytes(ids, dev), _is_bf16(Y, (T, weight.n_in), dev, "Y")
     _on(codes, dev, "codes")
-    st = f(ctypes.byref(weight.c_struct()), ids.data_ptr(), idb, T, scale, Y.data_ptr(), yb, _stream(stream))
+    st = f(ctypes.byref(weight.c_struct()), ids.data_ptr(), idb, T, scale, Y.data_ptr(), yb, _raw_stream(stream, dev))
     if st:
         _capi.check(name, st)
 
@@ -387,7 +392,7 @@ def qlora_embed_grad(ids: torch.Tensor, dY: torch.Tensor, scale: float, dE: torc
         _on(ws, dev, "ws")
     st = _lib().qlora_embed_grad(
         ids.data_ptr(), idb, T, dY.data_ptr(), yb, V, H, scale, padding_id, dE.data_ptr(), eb, 1 if accumulate else 0,
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(stream, dev))
     if st:
         _capi.check("qlora_embed_grad", st)
 
@@ -479,12 +484,13 @@ def qlora_adamw_plan_init(tensors, stream=None) -> AdamWPlan:
     tensors = list(tensors)
     if not tensors:
         raise ValueError("a plan needs a tensor")
+    dev = torch.cuda.current_device()
     arr = (_capi.AdamWTensorC * len(tensors))(*(t.c_struct() for t in tensors))
     nbytes = _lib().qlora_adamw_plan_bytes(arr, len(tensors))
     buffer = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device="cuda")
     plan = AdamWPlan(tensors, buffer, _capi.AdamWPlanC())
     _capi.check("qlora_adamw_plan_init", _lib().qlora_adamw_plan_init(arr, len(tensors), buffer.data_ptr(), buffer.numel(),
-                                                                      ctypes.byref(plan.c_plan), _stream(stream)))
+                                                                      ctypes.byref(plan.c_plan), _raw_stream(stream, dev)))
     return plan
 
 
@@ -503,7 +509,7 @@ def qlora_adamw_step(plan: AdamWPlan, lr: float, step: int, beta1: float = 0.9, 
     _on(plan.buffer, dev, "plan")
     st = _lib().qlora_adamw_step(
         ctypes.byref(plan.c_plan), lr, beta1, beta2, eps, step, _scalar(grad_scale, torch.float32, dev, "grad_scale"),
-        _scalar(lr_dev, torch.float32, dev, "lr_dev"), _scalar(step_dev, torch.int64, dev, "step_dev"), _stream(stream))
+        _scalar(lr_dev, torch.float32, dev, "lr_dev"), _scalar(step_dev, torch.int64, dev, "step_dev"), _raw_stream(stream, dev))
     if st:
         _capi.check("qlora_adamw_step", st)
 
@@ -513,7 +519,7 @@ def qlora_grad_norm(plan: AdamWPlan, max_norm: float, out: torch.Tensor, stream=
     dev = torch.cuda.current_device()
     _flat(out, 2, dev, _F32, "out")
     _on(plan.buffer, dev, "plan")
-    st = _lib().qlora_grad_norm(ctypes.byref(plan.c_plan), max_norm, out.data_ptr(), _stream(stream))
+    st = _lib().qlora_grad_norm(ctypes.byref(plan.c_plan), max_norm, out.data_ptr(), _raw_stream(stream, dev))
     if st:
         _capi.check("qlora_grad_norm", st)
 
@@ -523,20 +529,20 @@ def _adam8(codes, steps, x):
     kind = _capi.ADAM8_SECOND if _flat(codes, n, dev, (torch.int8, torch.uint8), "codes") is torch.uint8 else _capi.ADAM8_FIRST
     _flat(steps, (n + 255) // 256, dev, _F32, "steps")
     _flat(x, n, dev, _F32, "x")
-    return kind, n
+    return kind, n, dev
 
 
 def qlora_adam8_encode(x: torch.Tensor, codes: torch.Tensor, steps: torch.Tensor, stream=None) -> None:
     """8-bit state of float32 moments x: m into int8 codes, or v into uint8 codes (of its root), with block steps."""
-    kind, n = _adam8(codes, steps, x)
-    st = _lib().qlora_adam8_encode(x.data_ptr(), kind, codes.data_ptr(), steps.data_ptr(), n, _stream(stream))
+    kind, n, dev = _adam8(codes, steps, x)
+    st = _lib().qlora_adam8_encode(x.data_ptr(), kind, codes.data_ptr(), steps.data_ptr(), n, _raw_stream(stream, dev))
     if st:
         _capi.check("qlora_adam8_encode", st)
 
 
 def qlora_adam8_decode(codes: torch.Tensor, steps: torch.Tensor, x: torch.Tensor, stream=None) -> None:
     """The float32 moments that an 8-bit state stands for: m from int8 codes, v from uint8 codes."""
-    kind, n = _adam8(codes, steps, x)
-    st = _lib().qlora_adam8_decode(codes.data_ptr(), kind, steps.data_ptr(), x.data_ptr(), n, _stream(stream))
+    kind, n, dev = _adam8(codes, steps, x)
+    st = _lib().qlora_adam8_decode(codes.data_ptr(), kind, steps.data_ptr(), x.data_ptr(), n, _raw_stream(stream, dev))
     if st:
         _capi.check("qlora_adam8_decode", st)
