@@ -1191,6 +1191,50 @@ static qlora_status check_opt_tensors(const qlora_adamw_tensor *ts, int64_t coun
     return QLORA_OK;
 }
 
+// A run of device memory that a step reads or writes.
+struct MemRange {
+    uintptr_t lo, hi;
+    bool written;
+    int64_t tensor;
+};
+// Refuses a list whose written buffers overlap one another or a gradient: its elements would be updated
+// twice, or in an order that nothing fixes.  Gradients may share memory.
+static qlora_status check_opt_overlap(const qlora_adamw_tensor *ts, int64_t count) {
+    MemRange *r = static_cast<MemRange *>(std::malloc(size_t(count) * 7 * sizeof(MemRange)));
+    if (!r) return fail(QLORA_ERR_ARG, "no host memory for the plan");
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const qlora_adamw_tensor &t = ts[i];
+        if (t.numel == 0) continue;
+        const int64_t state = (t.flags & QLORA_OPT_STATE_8BIT) ? t.numel : 4 * t.numel, steps = 4 * ceil_div(t.numel, optim::kBlock);
+        auto add = [&](const void *p, int64_t bytes, bool written) {
+            const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+            if (p) r[n++] = MemRange{lo, lo + uintptr_t(bytes), written, i};
+        };
+        add(t.grad, t.numel * ((t.flags & QLORA_OPT_GRAD_BF16) ? 2 : 4), false);
+        if (t.flags & QLORA_OPT_GRAD_ONLY) continue;
+        add(t.param, t.numel * ((t.flags & QLORA_OPT_PARAM_BF16) ? 2 : 4), true);
+        add(t.param_bf16, t.numel * 2, true);
+        add(t.exp_avg, state, true);
+        add(t.exp_avg_sq, state, true);
+        if (t.flags & QLORA_OPT_STATE_8BIT) {
+            add(t.exp_avg_step, steps, true);
+            add(t.exp_avg_sq_step, steps, true);
+        }
+    }
+    std::sort(r, r + n, [](const MemRange &a, const MemRange &b) { return a.lo < b.lo; });
+    uintptr_t end_read = 0, end_written = 0;
+    int64_t bad = -1;
+    for (int64_t i = 0; i < n && bad < 0; ++i) {
+        if (r[i].lo < end_written || (r[i].written && r[i].lo < end_read)) bad = r[i].tensor;
+        uintptr_t &end = r[i].written ? end_written : end_read;
+        end = std::max(end, r[i].hi);
+    }
+    std::free(r);
+    if (bad >= 0) return fail(QLORA_ERR_ARG, "tensor %lld: a buffer overlaps one that the step writes", (long long)bad);
+    return QLORA_OK;
+}
+
 static int64_t plan_chunks(const qlora_adamw_tensor *ts, int64_t count, int64_t chunk) {
     int64_t n = 0;
     for (int64_t i = 0; i < count; ++i) n += ceil_div(ts[i].numel, chunk);
@@ -1209,6 +1253,7 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     *plan = qlora_adamw_plan{};
     int64_t numel = 0;
     QL_TRY(check_opt_tensors(tensors, count, &numel));
+    QL_TRY(check_opt_overlap(tensors, count));
     const int64_t chunk = plan_chunk(numel), nchunks = plan_chunks(tensors, count, chunk);
     if (nchunks > (1 << 30)) return fail(QLORA_ERR_SHAPE, "the tensors have too many elements for one plan");
     const size_t need = sizeof(optim::PlanHead) + size_t(nchunks) * sizeof(optim::Chunk);

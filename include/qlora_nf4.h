@@ -345,7 +345,8 @@ enum {
 };
 
 /* One tensor of a plan (80 bytes).  Buffers are contiguous device memory owned by
- * the caller, 16-byte aligned (block steps: 4 bytes); tensors must not overlap.
+ * the caller, 16-byte aligned (block steps: 4 bytes).  What a step writes must not
+ * overlap anything else of the plan; gradients may share memory.
  * numel = 0 is an empty tensor, whose pointers are not looked at. */
 typedef struct {
     void *param;            /* float32 or bfloat16 [numel], updated in place                  */

@@ -276,6 +276,23 @@ def test_grad_captured_and_replayed_with_new_ids():
         _check_grad(ids, dY, V, 1.0, -1, dE, None, how)
 
 
+@pytest.mark.parametrize("n", [5000, 131_073])
+def test_grad_of_larger_sorts_captured(n):
+    g = torch.Generator().manual_seed(n)
+    V, H = 3000, 16
+    ids, dY = _ids(g, n, V, "zipf").to(DEV), torch.randn(n, H, generator=g).to(DEV)
+    dE, ws = torch.empty(V, H, device=DEV), torch.empty(q.qlora_embed_grad_workspace_bytes(n, V, H), dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.qlora_embed_grad(ids, dY, 1.0, dE, ws=ws)
+        q.qlora_embed_grad(ids, dY, 1.0, dE, accumulate=True, ws=ws)
+    for _ in range(3):
+        graph.replay()
+    want, mag, cnt = T.embed_grad(ids.cpu(), dY.cpu().numpy(), V, 1.0)
+    tol = 2 * (cnt[:, None] + 1) * 2.0 ** -24 * (1 + 2.0 ** -10) * mag + 2.0 ** -23 * np.abs(2 * want)
+    assert (np.abs(dE.double().cpu().numpy() - 2 * want) <= tol).all()
+
+
 def test_two_gradients_at_once_on_two_streams():
     g = torch.Generator().manual_seed(25)
     V, H, n = 5000, 1024, 6000

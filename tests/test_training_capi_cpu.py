@@ -91,9 +91,10 @@ def test_embed_grad_workspace(lib):
     assert _grad(lib, wsb=n - 1) == WORKSPACE
 
 
-def _tensor(**kw):
-    t = dict(param=0x1000, grad=0x2000, exp_avg=0x3000, exp_avg_sq=0x4000, numel=1000, lr_scale=1.0, weight_decay=0.0,
-             flags=0)
+def _tensor(at=0, **kw):
+    t = dict(param=0x10000, grad=0x20000, exp_avg=0x30000, exp_avg_sq=0x40000, numel=1000, lr_scale=1.0,
+             weight_decay=0.0, flags=0)
+    t = {k: v + at if k in ("param", "grad", "exp_avg", "exp_avg_sq") else v for k, v in t.items()}
     t.update(kw)
     return _capi.AdamWTensorC(**t)
 
@@ -124,11 +125,37 @@ def test_plan_bytes_count_chunks(lib):
     (dict(weight_decay=float("inf")), ARG, "weight_decay"),
 ])
 def test_plan_refusals_name_the_tensor(lib, kw, code, msg):
-    arr = (_capi.AdamWTensorC * 2)(_tensor(), _tensor(**kw))
+    arr = (_capi.AdamWTensorC * 2)(_tensor(), _tensor(0x100000, **kw))
     plan = _capi.AdamWPlanC()
-    st = lib.qlora_adamw_plan_init(arr, 2, P(0x100000), 1 << 30, ctypes.byref(plan), None)
+    st = lib.qlora_adamw_plan_init(arr, 2, P(0x1000000), 1 << 30, ctypes.byref(plan), None)
     assert st == code and msg in _err(lib) and "tensor 1" in _err(lib), _err(lib)
     assert plan.magic == 0 and lib.qlora_adamw_plan_bytes(arr, 2) == 0
+
+
+STEPS = dict(flags=4, exp_avg_step=0x60000, exp_avg_sq_step=0x70000)
+
+
+@pytest.mark.parametrize("tensors,which", [
+    ([_tensor(), _tensor()], 1),                                             # the same tensor twice
+    ([_tensor(), _tensor(0x100000, param=0x10000 + 3984)], 1),               # one 16-byte word shared
+    ([_tensor(), _tensor(0x100000, grad=0x30000)], 1),                       # a gradient in another's state
+    ([_tensor(exp_avg_sq=0x30000)], 0),                                      # one state for both moments
+    ([_tensor(param_bf16=0x20010)], 0),                                      # the copy in the gradient
+    ([_tensor(exp_avg_step=0x60000, exp_avg_sq_step=0x6000c, flags=4)], 0),  # overlapping block steps
+    ([_tensor(**STEPS), _tensor(0x100000, **STEPS)], 1),
+])
+def test_overlapping_buffers_are_refused(lib, tensors, which):
+    arr = (_capi.AdamWTensorC * len(tensors))(*tensors)
+    plan = _capi.AdamWPlanC()
+    st = lib.qlora_adamw_plan_init(arr, len(tensors), P(0x1000000), 1 << 30, ctypes.byref(plan), None)
+    assert st == ARG and "overlaps" in _err(lib) and f"tensor {which}" in _err(lib), _err(lib)
+
+
+def test_neighbouring_buffers_and_shared_gradients_are_not_refused(lib):
+    arr = (_capi.AdamWTensorC * 3)(_tensor(), _tensor(0x100000, param=0x10000 + 4000), _tensor(0x200000, grad=0x20000))
+    plan = _capi.AdamWPlanC()
+    st = lib.qlora_adamw_plan_init(arr, 3, P(0x1000000), 1 << 30, ctypes.byref(plan), None)
+    assert st not in (ARG, SHAPE, ALIGN, WORKSPACE), _err(lib)      # fails later, for want of a GPU
 
 
 def test_plan_buffer_refusals(lib):
