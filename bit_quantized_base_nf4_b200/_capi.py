@@ -47,7 +47,7 @@ class AdamWTensorC(ctypes.Structure):
 class AdamWPlanC(ctypes.Structure):
     _fields_ = [("buffer", ctypes.c_void_p), ("chunks", ctypes.c_int64), ("chunks32", ctypes.c_int64),
                 ("numel", ctypes.c_int64), ("grad_only", ctypes.c_int32), ("magic", ctypes.c_int32),
-                ("reserved", ctypes.c_int64)]
+                ("elem8", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 OPT_PARAM_BF16, OPT_GRAD_BF16, OPT_STATE_8BIT, OPT_GRAD_ONLY = 1, 2, 4, 8

@@ -209,34 +209,37 @@ __device__ __forceinline__ void block_step(float a, float top2, float &d, float 
 // nearest integer to an approximate sqrt(y - 1/4): relative errors of 2^-23 for w and for the root and 2^-24 for
 // the product put it within 255 * 1.75 * 2^-23 = 5.4e-5 (m: 127 * 1.25 * 2^-23 = 1.9e-5).  Only where that root lies
 // closer to a half is y formed exactly and the candidate checked against the borders: in 3 % (m: 1 %) of
-// the blocks, for the elements concerned.
+// the blocks, for the elements concerned.  (y - 1/4) / 4^8 (m: / 4^7) is in [0, 1), so one saturating
+// multiply-add clamps what is below 1/4, and a NaN, to zero.
 constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer in the low mantissa bits
+__device__ __forceinline__ float fma_sat(float a, float b, float c) {
+    float r;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 template <bool kSecond>
 __device__ __forceinline__ void encode8(const float *x, const float *w, float inv, bool exact, uint32_t *c) {
-    constexpr float kNear = kSecond ? 0.49994f : 0.499975f;
+    constexpr float kNear = kSecond ? 0.49994f : 0.499975f, kRoot = kSecond ? 256.f : 128.f;
     uint32_t t[8];
-    float e[8], off = exact ? 1.f : 0.f;
-    const uint64_t magic = pack2(kMagic, kMagic), minus = pack2(-1.f, -1.f);
+    float e[8];
+    // below 2^-100 the scaled reciprocal could lose bits
+    exact = exact || inv < 7.8886091e-31f;
+    float off = exact && inv > 0.f ? 1.f : 0.f;
+    const float scaled = inv * (1.f / (kRoot * kRoot));
+    const uint64_t root = pack2(kRoot, kRoot), magic = pack2(kMagic, kMagic);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-        float z0, z1;
-        if (kSecond) {
-            unpack2(fma2(pack2(w[i], w[i + 1]), pack2(inv, inv), pack2(-0.25f, -0.25f)), z0, z1);
-        } else {
-            z0 = fmaf(fabsf(x[i]), inv, -0.25f);
-            z1 = fmaf(fabsf(x[i + 1]), inv, -0.25f);
-        }
-        z0 = sqrt_approx<true>(fmaxf(z0, 0.f));
-        z1 = sqrt_approx<true>(fmaxf(z1, 0.f));
+        float z0 = sqrt_approx<true>(fma_sat(kSecond ? w[i] : fabsf(x[i]), scaled, -0.25f / (kRoot * kRoot)));
+        float z1 = sqrt_approx<true>(fma_sat(kSecond ? w[i + 1] : fabsf(x[i + 1]), scaled, -0.25f / (kRoot * kRoot)));
         if (!kSecond) {
             z0 = copysignf(z0, x[i]);
             z1 = copysignf(z1, x[i + 1]);
         }
-        const uint64_t z = pack2(z0, z1), r = add2(z, magic);
+        const uint64_t z = pack2(z0, z1), r = fma2(z, root, magic);
         float r0, r1;
-        unpack2(add2(z, fma2(r, minus, magic)), e[i], e[i + 1]);    // z - (r - magic)
-        off = fmaxf(off, fmaxf(fabsf(e[i]), fabsf(e[i + 1])));
         unpack2(r, r0, r1);
+        unpack2(fma2(z, root, pack2(kMagic - r0, kMagic - r1)), e[i], e[i + 1]);    // root z - (r - magic)
+        off = fmaxf(off, fmaxf(fabsf(e[i]), fabsf(e[i + 1])));
         t[i] = __float_as_uint(r0);
         t[i + 1] = __float_as_uint(r1);
     }
@@ -433,20 +436,20 @@ __global__ void __launch_bounds__(kThreads, 4) adamw32_kernel(const StepArgs a) 
     }
 }
 
-// ---- 8-bit states: 10 to 18 bytes per parameter.  The codes cost about 45 instructions per parameter, so
-// instruction issue and HBM take about equally long, and a block's dependent chain (absmax, division, root,
-// code) is as long as a load.  So each warp streams its blocks through a ring of three in shared memory by
-// asynchronous copies, two blocks ahead of the one it works on.  A lane copies exactly what it reads
+// ---- 8-bit states: 10 to 18 bytes per parameter.  The codes cost some 50 instructions per parameter, so
+// instruction issue takes longer than HBM, and a block's dependent chain (absmax, division, root, code) is as
+// long as a load.  So each warp streams its elements through two stages of 512 in shared memory by
+// asynchronous copies, one stage ahead of the two blocks it works on.  A lane copies exactly what it reads
 // back itself, so the ring needs no barrier; copies past a tensor's end are zero-filled.
-constexpr int kStages = 3;
-constexpr int kStageBytes = kBlock * (4 + 4 + 1 + 1);      // g, p, m, v
-constexpr int kSlots = 4;                                  // chunks between the block worked on and the one copied
+constexpr int kUnit = 2 * kBlock;
+constexpr int kSlots = 4;                                  // chunks between the unit worked on and the one copied
 // A chunk at hand, in the warp's shared memory: the list's 80 bytes, and its rate and decay as pairs.
 struct alignas(16) Slot {
     Chunk c;
     uint64_t minus_lr, decay;
 };
-constexpr int kStep8Smem = kWarps * (kStages * kStageBytes + kSlots * int(sizeof(Slot)));
+// elem: bytes of g, p, m and v of the plan's widest element (6, 8 or 10)
+constexpr int step8_smem(int elem) { return kWarps * (2 * kUnit * elem + kSlots * int(sizeof(Slot))); }
 
 template <int kBytes>
 __device__ __forceinline__ void copy_async(uint32_t dst, uint64_t src) {
@@ -460,29 +463,32 @@ __device__ __forceinline__ void copy_async_part(uint32_t dst, uint64_t src, int 
     else if (kBytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// a lane's two runs of four elements (kSize bytes each) of the block at i0, of which rem elements are there
+// a lane's four runs of four elements (kSize bytes each) of the unit at i0, of which rem elements are there
 template <int kSize>
 __device__ __forceinline__ void copy_runs(uint32_t dst, uint64_t base, int i0, int rem, int lane) {
     const uint64_t src = base + static_cast<uint32_t>((i0 + lane * 4) * kSize);
     dst += lane * 4 * kSize;
-    if (rem >= kBlock) {
-        copy_async<4 * kSize>(dst, src);
-        copy_async<4 * kSize>(dst + 128 * kSize, src + 128 * kSize);
+    if (rem >= kUnit) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) copy_async<4 * kSize>(dst + h * 128 * kSize, src + h * 128 * kSize);
     } else {
-        rem -= lane * 4;
-        copy_async_part<4 * kSize>(dst, src, kSize * min(max(rem, 0), 4));
-        copy_async_part<4 * kSize>(dst + 128 * kSize, src + 128 * kSize, kSize * min(max(rem - 128, 0), 4));
+        // a run past the end reads nothing, so its address may lie anywhere
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            copy_async_part<4 * kSize>(dst + h * 128 * kSize, src + h * 128 * kSize, kSize * min(max(rem - lane * 4 - h * 128, 0), 4));
     }
 }
-__device__ __forceinline__ void copy_block(const Chunk &c, uint32_t stage, int i0, int lane) {
+__device__ __forceinline__ void copy_unit(const Chunk &c, uint32_t stage, int i0, int lane) {
     const int rem = c.n - i0;
     const uint32_t flags = c.flags;
     if (flags & kGradBf16) copy_runs<2>(stage, c.g, i0, rem, lane);
     else copy_runs<4>(stage, c.g, i0, rem, lane);
-    if (flags & kParamBf16) copy_runs<2>(stage + 4 * kBlock, c.p, i0, rem, lane);
-    else copy_runs<4>(stage + 4 * kBlock, c.p, i0, rem, lane);
-    copy_runs<1>(stage + 8 * kBlock, c.m, i0, rem, lane);
-    copy_runs<1>(stage + 9 * kBlock, c.v, i0, rem, lane);
+    stage += (flags & kGradBf16) ? 2 * kUnit : 4 * kUnit;
+    if (flags & kParamBf16) copy_runs<2>(stage, c.p, i0, rem, lane);
+    else copy_runs<4>(stage, c.p, i0, rem, lane);
+    stage += (flags & kParamBf16) ? 2 * kUnit : 4 * kUnit;
+    copy_runs<1>(stage, c.m, i0, rem, lane);
+    copy_runs<1>(stage + kUnit, c.v, i0, rem, lane);
 }
 // pairs 2 h and 2 h + 1 of a lane's elements of a parameter or gradient in a stage
 template <bool kBf16>
@@ -499,23 +505,25 @@ __device__ __forceinline__ void stage_pairs(const uint8_t *base, int h, int lane
     }
 }
 
+// One block: i0 its place in the chunk, g / p / mc / vc its parts of the stage, d its steps before (even lanes: m's,
+// odd lanes: sqrt(v)'s; replaced by the new ones).
 template <bool kPBf16, bool kGBf16, bool kFull>
-__device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s, const Slot &c, const uint8_t *stage, float dm,
-                                            float dv, int i0, int lane) {
+__device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s, const Slot &c, const uint8_t *g, const uint8_t *p,
+                                            const uint8_t *mc, const uint8_t *vc, float dm, float dv, float &d, int i0, int lane) {
     const int rem = c.c.n - i0;
     float mf[8], vf[8], w[8], pf[8];
     uint64_t m[4], v[4], x[2];
     uint32_t cm[2], cv[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        cm[h] = *reinterpret_cast<const uint32_t *>(stage + 8 * kBlock + h * 128 + lane * 4);
-        cv[h] = *reinterpret_cast<const uint32_t *>(stage + 9 * kBlock + h * 128 + lane * 4);
+        cm[h] = *reinterpret_cast<const uint32_t *>(mc + h * 128 + lane * 4);
+        cv[h] = *reinterpret_cast<const uint32_t *>(vc + h * 128 + lane * 4);
     }
     decode8<false>(cm, dm, m);
     decode8<true>(cv, dv, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (i % 2 == 0) stage_pairs<kGBf16>(stage, i / 2, lane, x);
+        if (i % 2 == 0) stage_pairs<kGBf16>(g, i / 2, lane, x);
         moments(a, s, x[i % 2], m[i], v[i]);
         unpack2(m[i], mf[2 * i], mf[2 * i + 1]);
         unpack2(v[i], vf[2 * i], vf[2 * i + 1]);
@@ -524,7 +532,7 @@ __device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s,
     const uint64_t minus_lr = c.minus_lr, decay = c.decay;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (i % 2 == 0) stage_pairs<kPBf16>(stage + 4 * kBlock, i / 2, lane, x);
+        if (i % 2 == 0) stage_pairs<kPBf16>(p, i / 2, lane, x);
         unpack2(update(s, minus_lr, decay, x[i % 2], m[i], w[2 * i], w[2 * i + 1]), pf[2 * i], pf[2 * i + 1]);
     }
     store8<kFull>(c.c.p, kPBf16, i0, rem, lane, pf);
@@ -542,28 +550,43 @@ __device__ __forceinline__ void step8_block(const StepArgs &a, const Scalars &s,
     // the root is monotonic, so the largest root is the root of the largest v; even lanes work out m's
     // step and odd lanes sqrt(v)'s
     const bool odd = lane & 1;
-    float d, inv;
+    float inv;
     block_step(odd ? __fsqrt_rn(av) : am, odd ? float(kTopW * kTopW) : float(kTopM * kTopM), d, inv);
     encode8<false>(mf, nullptr, __shfl_sync(0xffffffffu, inv, 0), false, cm);
     // below 2^-92 a flushed root could have had a code above 0
     encode8<true>(vf, w, __shfl_sync(0xffffffffu, inv, 1), s.flush && av < 2.0194839e-28f, cv);
     store_codes<kFull>(c.c.m, i0, rem, lane, cm);
     store_codes<kFull>(c.c.v, i0, rem, lane, cv);
-    if (lane < 2) reinterpret_cast<float *>(lane ? c.c.dv : c.c.dm)[i0 / kBlock] = d;
 }
+// The unit at i0 of a chunk; steps: in lanes 0 .. 3 the steps before of (m, sqrt(v)) of its two blocks.
 template <bool kPBf16, bool kGBf16>
-__device__ __forceinline__ void step8_any(const StepArgs &a, const Scalars &s, const Slot &c, const uint8_t *stage, float dm,
-                                          float dv, int i0, int lane) {
-    if (c.c.n - i0 >= kBlock) step8_block<kPBf16, kGBf16, true>(a, s, c, stage, dm, dv, i0, lane);
-    else step8_block<kPBf16, kGBf16, false>(a, s, c, stage, dm, dv, i0, lane);
+__device__ __forceinline__ void step8_unit(const StepArgs &a, const Scalars &s, const Slot &c, const uint8_t *stage, float steps,
+                                           int i0, int lane) {
+    constexpr int kG = kGBf16 ? 2 : 4, kP = kPBf16 ? 2 : 4;
+    const int blocks = min((c.c.n - i0 + kBlock - 1) / kBlock, 2);
+    float out = 0.f;
+#pragma unroll 1
+    for (int b = 0; b < blocks; ++b) {
+        const float dm = __shfl_sync(0xffffffffu, steps, 2 * b), dv = __shfl_sync(0xffffffffu, steps, 2 * b + 1);
+        const uint8_t *g = stage + b * (kBlock * kG), *p = stage + kUnit * kG + b * (kBlock * kP),
+                      *mc = stage + kUnit * (kG + kP) + b * kBlock, *vc = mc + kUnit;
+        float d;
+        if (c.c.n - i0 - b * kBlock >= kBlock)
+            step8_block<kPBf16, kGBf16, true>(a, s, c, g, p, mc, vc, dm, dv, d, i0 + b * kBlock, lane);
+        else
+            step8_block<kPBf16, kGBf16, false>(a, s, c, g, p, mc, vc, dm, dv, d, i0 + b * kBlock, lane);
+        if ((lane >> 1) == b) out = d;
+    }
+    if (lane < 2 * blocks) reinterpret_cast<float *>((lane & 1) ? c.c.dv : c.c.dm)[i0 / kBlock + (lane >> 1)] = out;
 }
 
 constexpr int kCtas8 = 3;      // CTAs per SM that the registers are capped for
-__global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const __grid_constant__ StepArgs a) {
-    extern __shared__ __align__(16) uint8_t step8_smem[];
+__global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const __grid_constant__ StepArgs a, int elem) {
+    extern __shared__ __align__(16) uint8_t step8_smem_base[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint8_t *ring = step8_smem + warp * (kStages * kStageBytes);
-    Slot *slots = reinterpret_cast<Slot *>(step8_smem + kWarps * kStages * kStageBytes) + warp * kSlots;
+    const int stage_bytes = kUnit * elem;
+    uint8_t *ring = step8_smem_base + warp * (2 * stage_bytes);
+    Slot *slots = reinterpret_cast<Slot *>(step8_smem_base + kWarps * 2 * stage_bytes) + warp * kSlots;
     const uint32_t ring_at = smem_u32(ring);
     const int stride = gridDim.x * kWarps;
     int done = blockIdx.x * kWarps + warp;                    // the chunk worked on
@@ -576,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const __grid_c
     Scalars s;
     if (!read_scalars(a, s)) return;
     int to_slot = 0, to_i0 = 0, to_stage = 0;
+    float next_steps = 0.f;
     // the chunk `ahead`, whose words are here, into slot to_slot; the words of the one after it are sent for
     auto open_slot = [&]() {
         const float lr = -(s.lr * __uint_as_float(word32(word, 16))), decay = __uint_as_float(word32(word, 17));
@@ -587,13 +611,14 @@ __global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const __grid_c
         if (ahead + stride < a.nchunks) word = chunk_word(a.chunks, ahead + stride, lane);
     };
     open_slot();
-    float next_dm = 0.f, next_dv = 0.f;
-    // starts the copies of the next block of the list, if there is one; every call closes one group
+    // starts the copies of the next unit of the list, if there is one, and loads its steps
     auto copy_next = [&]() {
         if (ahead < a.nchunks) {
             const Chunk &c = slots[to_slot].c;
-            copy_block(c, ring_at + to_stage * kStageBytes, to_i0, lane);
-            to_i0 += kBlock;
+            copy_unit(c, ring_at + to_stage * stage_bytes, to_i0, lane);
+            if (lane < 4 && to_i0 + (lane >> 1) * kBlock < c.n)
+                next_steps = reinterpret_cast<const float *>((lane & 1) ? c.dv : c.dm)[to_i0 / kBlock + (lane >> 1)];
+            to_i0 += kUnit;
             if (to_i0 >= c.n) {
                 to_i0 = 0;
                 ahead += stride;
@@ -601,41 +626,31 @@ __global__ void __launch_bounds__(kThreads, kCtas8) adamw8_kernel(const __grid_c
                 open_slot();
             }
         }
-        to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
+        to_stage ^= 1;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto steps_of = [&](const Chunk &c, int i0) {
-        next_dm = reinterpret_cast<const float *>(c.dm)[i0 / kBlock];
-        next_dv = reinterpret_cast<const float *>(c.dv)[i0 / kBlock];
-    };
-    copy_next();
     copy_next();
     int slot = 0, stage = 0, i0 = 0;
-    steps_of(slots[0].c, 0);
     while (true) {
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        const float steps = next_steps;
         copy_next();
         const Slot &c = slots[slot];
-        const float dm = next_dm, dv = next_dv;
-        // the block after this one
-        int n_slot = slot, n_i0 = i0 + kBlock;
-        if (n_i0 >= c.c.n) {
-            n_i0 = 0;
-            n_slot = (slot + 1) % kSlots;
-            done += stride;
-        }
-        if (done < a.nchunks) steps_of(slots[n_slot].c, n_i0);
-        const uint8_t *at = ring + stage * kStageBytes;
+        const uint8_t *at = ring + stage * stage_bytes;
         switch (c.c.flags & (kParamBf16 | kGradBf16)) {
-            case 0: step8_any<false, false>(a, s, c, at, dm, dv, i0, lane); break;
-            case kParamBf16: step8_any<true, false>(a, s, c, at, dm, dv, i0, lane); break;
-            case kGradBf16: step8_any<false, true>(a, s, c, at, dm, dv, i0, lane); break;
-            default: step8_any<true, true>(a, s, c, at, dm, dv, i0, lane);
+            case 0: step8_unit<false, false>(a, s, c, at, steps, i0, lane); break;
+            case kParamBf16: step8_unit<true, false>(a, s, c, at, steps, i0, lane); break;
+            case kGradBf16: step8_unit<false, true>(a, s, c, at, steps, i0, lane); break;
+            default: step8_unit<true, true>(a, s, c, at, steps, i0, lane);
         }
-        if (done >= a.nchunks) return;
-        stage = stage + 1 == kStages ? 0 : stage + 1;
-        slot = n_slot;
-        i0 = n_i0;
+        stage ^= 1;
+        i0 += kUnit;
+        if (i0 >= c.c.n) {
+            i0 = 0;
+            slot = (slot + 1) % kSlots;
+            done += stride;
+            if (done >= a.nchunks) return;
+        }
     }
 }
 

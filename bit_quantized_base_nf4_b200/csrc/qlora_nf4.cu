@@ -1269,7 +1269,7 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     // chunks of tensors with 32-bit states first, then those with 8-bit states: a kernel for each
     optim::Chunk *const list = reinterpret_cast<optim::Chunk *>(host + sizeof(optim::PlanHead)), *c = list;
     int64_t chunks32 = 0;
-    int32_t grad_only = 0;
+    int32_t grad_only = 0, elem8 = 0;
     for (int pass = 0; pass < 2; ++pass) {
         for (int64_t i = 0; i < count; ++i) {
             const qlora_adamw_tensor &t = tensors[i];
@@ -1278,6 +1278,7 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
             if (only && t.numel) grad_only = 1;
             const int64_t pb = (t.flags & QLORA_OPT_PARAM_BF16) ? 2 : 4, gb = (t.flags & QLORA_OPT_GRAD_BF16) ? 2 : 4, sb = eight ? 1 : 4;
             auto at = [](const void *base, int64_t off) { return base ? uint64_t(reinterpret_cast<uintptr_t>(base)) + uint64_t(off) : 0; };
+            if (eight && t.numel) elem8 = std::max(elem8, static_cast<int32_t>(gb + pb + 2));
             for (int64_t e = 0; e < t.numel; e += chunk, ++c) {
                 c->g = at(t.grad, e * gb);
                 c->n = static_cast<int32_t>(std::min(chunk, t.numel - e));
@@ -1304,6 +1305,7 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     plan->chunks32 = chunks32;
     plan->numel = numel;
     plan->grad_only = grad_only;
+    plan->elem8 = elem8;
     plan->magic = kPlanMagic;
     return QLORA_OK;
 }
@@ -1371,9 +1373,11 @@ qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double be
     if (plan->chunks > plan->chunks32) {
         a.chunks = plan_list(plan) + plan->chunks32;
         a.nchunks = static_cast<int>(plan->chunks - plan->chunks32);
-        QL_TRY(set_smem(optim::adamw8_kernel, optim::kStep8Smem));
-        QL_TRY(launch_pdl("adamw8_kernel launch", optim::adamw8_kernel, plan_grid(a.nchunks, optim::kCtas8), optim::kThreads,
-                          optim::kStep8Smem, st, a));
+        // the stages of three CTAs fit an SM's shared memory up to 8 bytes an element, of two at 10
+        const int smem = optim::step8_smem(plan->elem8);
+        QL_TRY(set_smem(optim::adamw8_kernel, optim::step8_smem(10)));
+        QL_TRY(launch_pdl("adamw8_kernel launch", optim::adamw8_kernel, plan_grid(a.nchunks, plan->elem8 > 8 ? 2 : optim::kCtas8),
+                          optim::kThreads, smem, st, a, int(plan->elem8)));
     }
     return QLORA_OK;
 }

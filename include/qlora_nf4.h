@@ -369,8 +369,7 @@ typedef struct {
 typedef struct {
     void *buffer;
     int64_t chunks, chunks32, numel;
-    int32_t grad_only, magic;
-    int64_t reserved;
+    int32_t grad_only, magic, elem8, reserved;
 } qlora_adamw_plan;
 
 /* Bytes of the plan buffer for these tensors (host arithmetic only); 0 for a list
