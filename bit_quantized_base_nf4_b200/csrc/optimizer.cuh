@@ -226,7 +226,7 @@ __device__ __forceinline__ void encode8(const float *x, const float *w, float in
     exact = exact || inv < 7.8886091e-31f;
     float off = exact && inv > 0.f ? 1.f : 0.f;
     const float scaled = inv * (1.f / (kRoot * kRoot));
-    const uint64_t root = pack2(kRoot, kRoot), magic = pack2(kMagic, kMagic);
+    const uint64_t root = pack2(kRoot, kRoot), magic = pack2(kMagic, kMagic), minus = pack2(-1.f, -1.f);
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         float z0 = sqrt_approx<true>(fma_sat(kSecond ? w[i] : fabsf(x[i]), scaled, -0.25f / (kRoot * kRoot)));
@@ -238,7 +238,7 @@ __device__ __forceinline__ void encode8(const float *x, const float *w, float in
         const uint64_t z = pack2(z0, z1), r = fma2(z, root, magic);
         float r0, r1;
         unpack2(r, r0, r1);
-        unpack2(fma2(z, root, pack2(kMagic - r0, kMagic - r1)), e[i], e[i + 1]);    // root z - (r - magic)
+        unpack2(fma2(z, root, fma2(r, minus, magic)), e[i], e[i + 1]);    // root z - (r - magic)
         off = fmaxf(off, fmaxf(fabsf(e[i]), fabsf(e[i + 1])));
         t[i] = __float_as_uint(r0);
         t[i + 1] = __float_as_uint(r1);
