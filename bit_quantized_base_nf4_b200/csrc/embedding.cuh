@@ -304,13 +304,15 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t n, uint32_t *wsum, int
     return base + incl - n;
 }
 
-// Radix sort, least significant digit first, by one CTA (up to 4096 tokens) or by the cluster of kSortCtas (up to
-// 131072), with a CTA's tokens in registers.  Tokens are dealt in order to CTAs, warps and rounds of 32, so a
+// Radix sort, least significant digit first, by one CTA (up to 2048 tokens) or by the cluster of kSortCtas (up to
+// 131072), with a CTA's tokens in registers.  Whole gradient of rows of 64, one CTA / cluster: 11.4 / 14.4 us at 1024
+// tokens, 15.0 / 15.9 at 2048, 20.2 / 17.5 at 4096; held in registers / swept from memory (below): 34.9 / 40.4 us
+// at 32768, 89.7 / 96.5 at 131072.  Tokens are dealt in order to CTAs, warps and rounds of 32, so a
 // token's place among equal digits is the count in lower CTAs, in lower warps, in its warp's earlier rounds and
 // in its lower lanes: stable without atomics.  A CTA reorders its tokens in shared memory first, so that what it
 // writes to global memory comes in runs (scattered 4-byte stores kept one SM busy for 25 us per 16384 tokens).
 constexpr int kCtaRounds = 16;                       // most rounds of 1024 tokens a CTA holds
-constexpr int kOneTokens = 4 * kSortThreads;
+constexpr int kOneTokens = 2 * kSortThreads;
 constexpr int kHeldTokens = kCtaRounds * kSortThreads * kSortCtas;
 constexpr int kHeldWords = kSortWarps * kMaxBins + 4 * kMaxBins + 64;
 constexpr int held_smem(int rounds) { return 4 * kHeldWords + 8 * kSortThreads * rounds; }

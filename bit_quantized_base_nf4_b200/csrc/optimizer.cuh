@@ -32,7 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPartials = 4096;      // most CTAs of the norm: slots for their partial sums
 constexpr int kTopM = 127, kTopW = 255;
 
-enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2, kState8 = 4 };
+enum : uint32_t { kParamBf16 = 1, kGradBf16 = 2 };
 
 // A run of at most `chunk` elements of one tensor, starting at a multiple of kBlock: the
 // addresses of its first element in every buffer.  80 bytes; a warp loads it with one
@@ -64,37 +64,7 @@ __device__ __forceinline__ uint64_t word64(uint32_t w, int i) {
 }
 
 // Element of half h (0, 1) and place j (0..3) of a lane's 8 in a block: h * 128 + lane * 4 + j.
-__device__ __forceinline__ void unpack4(uint2 u, float *x) {
-    x[0] = __uint_as_float(u.x << 16);
-    x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(u.y << 16);
-    x[3] = __uint_as_float(u.y & 0xFFFF0000u);
-}
 // rem: elements of the chunk from the block's first on.  kFull: rem >= 256.
-template <bool kFull>
-__device__ __forceinline__ void load8(uint64_t base, bool bf16, int64_t i0, int rem, int lane, float *x) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int e = h * 128 + lane * 4;
-        if (kFull) {
-            if (bf16) {
-                unpack4(*reinterpret_cast<const uint2 *>(base + 2 * (i0 + e)), x + 4 * h);
-            } else {
-                const float4 f = *reinterpret_cast<const float4 *>(base + 4 * (i0 + e));
-                x[4 * h] = f.x, x[4 * h + 1] = f.y, x[4 * h + 2] = f.z, x[4 * h + 3] = f.w;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float f = 0.f;
-                if (e + j < rem)
-                    f = bf16 ? __uint_as_float(uint32_t(reinterpret_cast<const uint16_t *>(base)[i0 + e + j]) << 16)
-                             : reinterpret_cast<const float *>(base)[i0 + e + j];
-                x[4 * h + j] = f;
-            }
-        }
-    }
-}
 template <bool kFull>
 __device__ __forceinline__ void store8(uint64_t base, bool bf16, int64_t i0, int rem, int lane, const float *x) {
 #pragma unroll
@@ -680,7 +650,8 @@ __device__ __forceinline__ double norm_chunk(uint64_t g, int n, int lane, double
     }
     for (; i0 < n; i0 += kBlock) {
         Raw8<kBf16> x;
-        x.template load<false>(g, i0, n - i0, lane);
+        if (n - i0 >= kBlock) x.template load<true>(g, i0, kBlock, lane);
+        else x.template load<false>(g, i0, n - i0, lane);
         sum = sum_squares<kBf16>(x.w, sum);
     }
     return sum;
@@ -746,13 +717,14 @@ __global__ void __launch_bounds__(kThreads) adam8_encode_kernel(const float *x, 
     for (int64_t b = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5); b < nblk; b += int64_t(gridDim.x) * kWarps) {
         const int rem = static_cast<int>(n - b * kBlock < kBlock ? n - b * kBlock : kBlock);
         const uint64_t src = reinterpret_cast<uint64_t>(x), dst = reinterpret_cast<uint64_t>(codes);
-        float f[8];
-        if (rem == kBlock) load8<true>(src, false, b * kBlock, rem, lane, f);
-        else load8<false>(src, false, b * kBlock, rem, lane, f);
+        Raw8<false> raw;
+        if (rem == kBlock) raw.template load<true>(src, b * kBlock, rem, lane);
+        else raw.template load<false>(src, b * kBlock, rem, lane);
         uint32_t c[2];
-        float w[8], top = 0.f, d, inv;
+        float f[8], w[8], top = 0.f, d, inv;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            f[i] = __uint_as_float(raw.w[i]);
             w[i] = 0.f;
             if (kSecond) {
                 w[i] = sqrt_approx<false>(f[i]);

@@ -1002,8 +1002,11 @@ static qlora_status launch_embed_fwd(emb::FwdArgs &a, const void *ids, int ids_b
     const int64_t gy = ceil_div(segs, int64_t(1) << a.seg_shift), per_pass = emb::kFwdWarps >> a.seg_shift;
     if (gy > 65535) return fail(QLORA_ERR_SHAPE, "the row length (%lld) is too large", (long long)H);
     QL_TRY(require_sm100());
-    // several tokens a warp once the batch fills the device (8 CTAs per SM) four times over
-    a.passes = ceil_div(T, per_pass) * gy >= int64_t(sm_count()) * 8 * emb::kFwdPasses ? emb::kFwdPasses : 1;
+    // Tokens a warp takes one after the other: table set-up and id loads are shared, but a small batch then
+    // leaves SMs idle.  1 / 2 / 4 tokens, 4-bit table: 4.3 / 5.3 / 7.7 us at 2048 x 4096 (1024 CTAs of one token a
+    // warp), 16.7 / 15.8 / 16.6 at 4096 x 8192 (4096 CTAs), 58.5 / 53.2 / 52.1 at 16384 x 8192.
+    const int64_t ctas = ceil_div(T, per_pass) * gy, full = int64_t(sm_count()) * 8;
+    a.passes = ctas >= 8 * full ? emb::kFwdPasses : ctas >= 2 * full ? 2 : 1;
     a.ids = emb::Ids{ids, ids_bytes == 8};
     a.out = Y;
     a.T = T;
@@ -1051,8 +1054,10 @@ qlora_status qlora_embed_fwd(const void *E, int e_is_bf16, int64_t V, int64_t H,
     return launch_embed_fwd<emb::kTableF32, false>(a, ids, ids_bytes, T, V, H, scale, Y, y_is_bf16, stream);
 }
 
-// Sorted tokens per chunk of the gradient's reduction: a power of two in [8, 64], about eight blocks per
-// SM (148) where T allows it; longer chunks leave fewer partial sums, shorter ones more blocks.
+// Sorted tokens per chunk of the gradient's reduction: a power of two in [8, 128], about eight blocks per
+// SM (148) where T allows it; longer chunks leave fewer partial sums, shorter ones more blocks.  Added, bf16 to
+// fp32, chunks of 8 / 16 / 32 / 64 / 128: 24 / 29 / 29 / 30 / 41 us at 2047 x 4096, 52 / 51 / 52 / 61 / 69 at 8192 x 4096,
+// 285 / 235 / 212 / 202 / 200 at 32768 x 8192; the rule takes 8, 16 and 128.
 static int embed_chunk(int64_t T, int64_t H) {
     const int64_t want = T * ceil_div(H, emb::kRedCols) / (8 * 148);
     int c = 8;
@@ -1113,7 +1118,7 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
             const bool one = T <= emb::kOneTokens;
             const int rounds = static_cast<int>(ceil_div(T, int64_t(one ? 1 : emb::kSortCtas) * emb::kSortThreads));
             void (*sort)(emb::GradArgs, int);
-            if (one) sort = rounds == 1 ? emb::embed_sort_one_kernel<1> : emb::embed_sort_one_kernel<4>;
+            if (one) sort = rounds == 1 ? emb::embed_sort_one_kernel<1> : emb::embed_sort_one_kernel<2>;
             else if (rounds <= 2) sort = emb::embed_sort_held_kernel<2>;
             else sort = rounds <= 4 ? emb::embed_sort_held_kernel<4> : emb::embed_sort_held_kernel<emb::kCtaRounds>;
             QL_TRY(set_smem(sort, emb::held_smem(rounds)));
@@ -1152,9 +1157,10 @@ static_assert(sizeof(qlora_adamw_plan) == 48, "ABI layout");
 constexpr int32_t kOptFlags = QLORA_OPT_PARAM_BF16 | QLORA_OPT_GRAD_BF16 | QLORA_OPT_STATE_8BIT | QLORA_OPT_GRAD_ONLY;
 constexpr int32_t kPlanMagic = 0x51504c4e;
 
-// Elements of a plan's chunk for `numel` in all: the largest multiple of 256 from 256 to 1024 that still
-// gives every warp of the device (64 per SM) a chunk.  A chunk's 80 bytes are 0.3 to 0.8 % of the bytes
-// of 1024 elements; the last round of a large plan's chunks leaves 1 to 2 % of the warps idle.
+// Elements of a plan's chunk for `numel` in all: the largest of 256, 512 and 1024 that still gives every warp of
+// the device (64 per SM) a chunk.  256 / 512 / 1024 / 2048: 2.9 / 3.1 / 4.6 / 7.1 us for a 32-bit step on 262 K parameters,
+// 36.8 / 31.1 / 33.1 / 37.4 for an 8-bit one (and its state read back) on 5.8 M, 144 / 147 / 149 / 153 and
+// 184 / 152 / 154 / 158 on 32 M, and 92 / 83 / 81 / 80 for the norm of 129 M gradients.
 static int64_t plan_chunk(int64_t numel) {
     int64_t c = 1024;
     while (c > 256 && numel / c < 64 * 148) c /= 2;
@@ -1373,7 +1379,8 @@ qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double be
     if (plan->chunks > plan->chunks32) {
         a.chunks = plan_list(plan) + plan->chunks32;
         a.nchunks = static_cast<int>(plan->chunks - plan->chunks32);
-        // the stages of three CTAs fit an SM's shared memory up to 8 bytes an element, of two at 10
+        // The stages of three CTAs fit an SM's shared memory up to 8 bytes an element, of two at 10.  One / two / three
+        // CTAs, 32 M parameters, state read back: 232 / 169 / 136 us at 6 bytes, 228 / 181 / 148 at 8, 225 / 153 at 10.
         const int smem = optim::step8_smem(plan->elem8);
         QL_TRY(set_smem(optim::adamw8_kernel, optim::step8_smem(10)));
         QL_TRY(launch_pdl("adamw8_kernel launch", optim::adamw8_kernel, plan_grid(a.nchunks, plan->elem8 > 8 ? 2 : optim::kCtas8),
