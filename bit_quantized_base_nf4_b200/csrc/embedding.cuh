@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const __grid_con
 //           and written, one that crosses a border leaves a partial sum per chunk;
 //   join    adds the partial sums of each such id in order and writes its row;
 //   zero    (unless the gradient is added) zeroes the other rows.
+// Up to kFewTokens tokens take one launch in place of the first three.
 // Every sum is float32, in an order fixed by the ids alone: results repeat bit for bit.
 // The last three overlap: each starts once the one before it has started (programmatic dependent
 // launch).  `zero` needs the sort only, so its writes, nearly all of the time when the table is large, run
@@ -512,28 +513,39 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
 // Zero: a CTA of 256 threads for about 16 KB of rows, in the order of the table.  (A grid of two CTAs per SM
 // that strides over the rows wrote 6.0 TB/s, this order 7.2: what is written at any time lies close together.)
 constexpr int kZeroThreads = 256;
+template <bool kFew>
 __global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(const GradArgs a) {
+    __shared__ uint32_t s_named[kFew ? 32 : 1];
     pdl_launch_dependents();
-    if (a.T == 0) pdl_wait();   // otherwise the reduction has let this kernel start, after its own wait for the sort
+    if (a.T == 0) pdl_wait();   // otherwise the kernel before has let this one start, after its own wait for ids and sort
     const int64_t row_words = a.H * (a.de_bf16 ? 2 : 4) / 16;
-    const int64_t end = min((blockIdx.x + int64_t(1)) * a.zero_rows, a.V);
+    const int64_t r0 = blockIdx.x * int64_t(a.zero_rows), end = min(r0 + a.zero_rows, a.V);
+    if (kFew) {                 // no sort has marked the rows: the CTA looks for its own among the few ids
+        if (threadIdx.x < 32) s_named[threadIdx.x] = 0;
+        __syncthreads();
+        for (int t = threadIdx.x; t < a.T; t += kZeroThreads) {
+            const int64_t id = id_at(a.ids, t);
+            if (id >= r0 && id < end && id != a.pad) atomicOr(s_named + ((id - r0) >> 5), 1u << ((id - r0) & 31));
+        }
+        __syncthreads();
+    }
+    auto named = [&](int64_t r) {
+        if (kFew) return (s_named[(r - r0) >> 5] >> ((r - r0) & 31)) & 1u;
+        return a.T > 0 ? (__ldcg(a.named + (r >> 5)) >> (r & 31)) & 1u : 0u;
+    };
     if (row_words >= kZeroThreads) {
-        for (int64_t r = blockIdx.x * int64_t(a.zero_rows); r < end; ++r) {
-            if (a.T > 0 && ((__ldcg(a.named + (r >> 5)) >> (r & 31)) & 1u)) continue;
+        for (int64_t r = r0; r < end; ++r) {
+            if (named(r)) continue;
             uint4 *dst = static_cast<uint4 *>(a.dE) + r * row_words;
 #pragma unroll 4
             for (int64_t i = threadIdx.x; i < row_words; i += kZeroThreads) dst[i] = make_uint4(0, 0, 0, 0);
         }
     } else {
-        // short rows: the CTA's words as one run (at most 1024 + 255 rows' words, 32-bit)
-        const int64_t r0 = blockIdx.x * int64_t(a.zero_rows);
+        // short rows: the CTA's words as one run (at most 1024, or one row's)
         const uint32_t words = static_cast<uint32_t>((end - r0) * row_words), rw = static_cast<uint32_t>(row_words);
         uint4 *dst = static_cast<uint4 *>(a.dE) + r0 * row_words;
-        for (uint32_t i = threadIdx.x; i < words; i += kZeroThreads) {
-            const int64_t r = r0 + i / rw;
-            if (a.T > 0 && ((__ldcg(a.named + (r >> 5)) >> (r & 31)) & 1u)) continue;
-            dst[i] = make_uint4(0, 0, 0, 0);
-        }
+        for (uint32_t i = threadIdx.x; i < words; i += kZeroThreads)
+            if (!named(r0 + i / rw)) dst[i] = make_uint4(0, 0, 0, 0);
     }
     if (blockIdx.x == gridDim.x - 1) pdl_wait();
 }
@@ -643,6 +655,65 @@ __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArg
             } else {
                 write_row<kDeBf16, 8>(a, id, c, acc, old[u]);
             }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+        }
+    }
+}
+
+// A few tokens (up to kFewTokens): one launch instead of sort, reduce and join.  Every block ranks the ids for
+// itself (a thread counts the smaller ones), and a group of blocks takes the ids that start in kFewRun
+// places of the sorted list, each to its end.
+constexpr int kFewTokens = kRedThreads;
+constexpr int kFewRun = 4;
+template <bool kDyBf16, bool kDeBf16, bool kAdd>
+__global__ void __launch_bounds__(kRedThreads) embed_few_kernel(const GradArgs a) {
+    __shared__ uint32_t s_key[kFewTokens], s_id[kFewTokens + 2], s_pos[kFewTokens];   // s_id as in embed_reduce_kernel
+    pdl_wait();                 // before the release: `zero` may rely on the ids
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, T = static_cast<int>(a.T);
+    const uint32_t V = static_cast<uint32_t>(a.V);
+    const uint32_t key = tid < T ? key_of(a, tid) : V;
+    s_key[tid] = key;
+    if (tid == 0) s_id[0] = s_id[T + 1] = 0xFFFFFFFFu;
+    __syncthreads();
+    if (tid < T) {
+        int place = 0;
+        for (int s = 0; s < T; ++s) place += s_key[s] < key || (s_key[s] == key && s < tid);
+        s_id[place + 1] = key;
+        s_pos[place] = tid;
+    }
+    __syncthreads();
+    int lo = blockIdx.x * kFewRun, hi = min(lo + kFewRun, T);
+    while (lo < hi && s_id[lo + 1] == s_id[lo]) ++lo;        // an id that starts before belongs to the block before
+    if (lo >= hi || s_id[lo + 1] >= V) return;
+    while (s_id[hi + 1] == s_id[hi]) ++hi;
+    const int64_t c = int64_t(blockIdx.y) * kRedCols + tid * 8;
+    if (c >= a.H) return;
+    float acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    for (int i = lo; i < hi; i += kBatch) {
+        Raw<kDyBf16, 8> r[kBatch];
+        Raw<kDeBf16, 8> old[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            old[u].zero();
+            if (i + u >= hi) continue;
+            const uint32_t id = s_id[i + u + 1];
+            if (id >= V) continue;
+            r[u].load(a.dY, int64_t(s_pos[i + u]) * a.H + c);
+            if (kAdd && s_id[i + u + 2] != id) old[u].load(a.dE, int64_t(id) * a.H + c);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (i + u >= hi) break;
+            const uint32_t id = s_id[i + u + 1];
+            if (id >= V) break;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += r[u].at(j);
+            if (s_id[i + u + 2] == id) continue;
+            write_row<kDeBf16, 8>(a, id, c, acc, old[u]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] = 0.f;
         }

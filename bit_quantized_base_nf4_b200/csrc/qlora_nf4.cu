@@ -1113,7 +1113,17 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
     if (jtiles > 65535) return fail(QLORA_ERR_SHAPE, "H (%lld) must be at most %d", (long long)H, 65535 * emb::kJoinCols);
     QL_TRY(require_sm100());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (T > 0) {
+    const int variant = 4 * dy_is_bf16 + 2 * de_is_bf16 + accumulate;
+    const bool few = T > 0 && T <= emb::kFewTokens;
+    if (few) {
+        void (*const sum[8])(emb::GradArgs) = {
+            emb::embed_few_kernel<false, false, false>, emb::embed_few_kernel<false, false, true>,
+            emb::embed_few_kernel<false, true, false>,  emb::embed_few_kernel<false, true, true>,
+            emb::embed_few_kernel<true, false, false>,  emb::embed_few_kernel<true, false, true>,
+            emb::embed_few_kernel<true, true, false>,   emb::embed_few_kernel<true, true, true>};
+        QL_TRY(launch_pdl("embed_few_kernel launch", sum[variant],
+                          dim3(static_cast<unsigned>(ceil_div(T, emb::kFewRun)), static_cast<unsigned>(tiles)), emb::kRedThreads, 0, st, a));
+    } else if (T > 0) {
         if (T <= emb::kHeldTokens) {
             const bool one = T <= emb::kOneTokens;
             const int rounds = static_cast<int>(ceil_div(T, int64_t(one ? 1 : emb::kSortCtas) * emb::kSortThreads));
@@ -1134,17 +1144,17 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
             emb::embed_reduce_kernel<false, true, false>,  emb::embed_reduce_kernel<false, true, true>,
             emb::embed_reduce_kernel<true, false, false>,  emb::embed_reduce_kernel<true, false, true>,
             emb::embed_reduce_kernel<true, true, false>,   emb::embed_reduce_kernel<true, true, true>};
-        QL_TRY(launch_pdl("embed_reduce_kernel launch", reduce[4 * dy_is_bf16 + 2 * de_is_bf16 + accumulate],
+        QL_TRY(launch_pdl("embed_reduce_kernel launch", reduce[variant],
                           dim3(static_cast<unsigned>(a.nchunks), static_cast<unsigned>(tiles)), emb::kRedThreads, 0, st, a));
-        if (a.nchunks > 1)
-            QL_TRY(launch_pdl("embed_join_kernel launch", de_is_bf16 ? emb::embed_join_kernel<true> : emb::embed_join_kernel<false>,
-                              dim3(static_cast<unsigned>(ceil_div(a.nchunks - 1, emb::kJoinWarps)), static_cast<unsigned>(jtiles)),
-                              emb::kJoinWarps * 32, 0, st, a));
+        // (more than kFewTokens tokens are more than one chunk)
+        QL_TRY(launch_pdl("embed_join_kernel launch", de_is_bf16 ? emb::embed_join_kernel<true> : emb::embed_join_kernel<false>,
+                          dim3(static_cast<unsigned>(ceil_div(a.nchunks - 1, emb::kJoinWarps)), static_cast<unsigned>(jtiles)),
+                          emb::kJoinWarps * 32, 0, st, a));
     }
     if (!accumulate) {
         // rows of about 16 KB a CTA
         a.zero_rows = static_cast<int>(std::min<int64_t>(V, std::max<int64_t>(1, 16384 / (H * (de_is_bf16 ? 2 : 4)))));
-        QL_TRY(launch_pdl("embed_zero_kernel launch", emb::embed_zero_kernel,
+        QL_TRY(launch_pdl("embed_zero_kernel launch", few ? emb::embed_zero_kernel<true> : emb::embed_zero_kernel<false>,
                           dim3(static_cast<unsigned>(ceil_div(V, a.zero_rows))), emb::kZeroThreads, 0, st, a));
     }
     return QLORA_OK;

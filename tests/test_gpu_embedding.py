@@ -155,6 +155,11 @@ GRAD = [
     (8, 40, 1032, "any", torch.float32, torch.bfloat16, False, -1, 1.0, torch.int64),
     (9, 511, 64, "one", torch.bfloat16, torch.float32, True, -1, -3.0, torch.int32),
     (33, 512, 136, "zipf", torch.float32, torch.float32, True, 0, 1.0, torch.int64),
+    (128, 40, 1160, "zipf", torch.bfloat16, torch.float32, False, 2, 1.0, torch.int64),
+    (128, 4096, 24, "one", torch.float32, torch.bfloat16, True, -1, 0.5, torch.int32),
+    (129, 40, 1160, "zipf", torch.bfloat16, torch.float32, False, 2, 1.0, torch.int64),
+    (101, 30_000, 4096, "any", torch.bfloat16, torch.float32, False, 0, 1.0, torch.int64),
+    (77, 3, 520, "runs", torch.bfloat16, torch.bfloat16, False, -1, 1.0, torch.int32),
     (1000, 513, 264, "zipf", torch.bfloat16, torch.float32, False, 0, 1.0, torch.int32),
     (1025, 40_000, 2056, "zipf", torch.bfloat16, torch.float32, False, -1, 1.0, torch.int64),
     (4097, 700, 128, "one", torch.bfloat16, torch.float32, False, -1, 1.0, torch.int64),
