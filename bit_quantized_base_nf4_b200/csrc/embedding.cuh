@@ -205,17 +205,19 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ gradient
-// dE[v, :] (+)= scale * sum over the tokens t with id_t = v of dY[t, :], in up to four launches:
-//   sort    the tokens by id (stable), and mark the rows that they name;
+// dE[v, :] (+)= scale * sum over the tokens t with id_t = v of dY[t, :], in three or five launches:
+//   mark    (unless the gradient is added) sets a bit for every row that a token names;
+//   sort    the tokens by id (stable);
 //   reduce  equal runs of `chunk` sorted tokens each: an id that lies wholly in a chunk is summed
 //           and written, one that crosses a border leaves a partial sum per chunk;
 //   join    adds the partial sums of each such id in order and writes its row;
-//   zero    (unless the gradient is added) zeroes the other rows.
-// Up to kFewTokens tokens take one launch in place of the first three.
+//   zero    (unless the gradient is added) zeroes the rows without a bit.
+// Up to kFewTokens tokens take one launch in place of the first four, and `zero` looks at the ids itself.
 // Every sum is float32, in an order fixed by the ids alone: results repeat bit for bit.
-// The last three overlap: each starts once the one before it has started (programmatic dependent
-// launch).  `zero` needs the sort only, so its writes, nearly all of the time when the table is large, run
-// beside the reduction; its last CTA waits for the join, so that its completion means the whole call's.
+// Programmatic dependent launch: a kernel starts once the one before it has started, and the sort is let
+// start before it waits for the marks but lets the others start only then.  So `zero`, whose writes are nearly all of the time
+// when the table is large, needs no wait of its own and runs beside the sort and the reduction; its last
+// CTA waits for the join, so that its completion means the whole call's.
 constexpr int kSortCtas = 8;            // one cluster sorts: bins and counts meet in shared memory
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -339,13 +341,6 @@ __device__ void sort_held(const GradArgs &a, uint32_t *smem, int rounds) {
         k[u] = t < n ? key_of(a, lo + t) : 0u;
         p[u] = static_cast<uint32_t>(lo + t);
     }
-    if (!a.accumulate) {
-#pragma unroll
-        for (int u = 0; u < kRounds; ++u) {
-            if (u >= rounds) break;
-            if (i0 + 32 * u < n && k[u] < a.V) atomicOr(a.named + (k[u] >> 5), 1u << (k[u] & 31));
-        }
-    }
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = pass * a.bits;
         for (int b = lane; b < bins; b += 32) my[b] = 0;
@@ -447,9 +442,7 @@ __device__ void sort_swept(const GradArgs &a, uint32_t *smem) {
                 }
             }
         };
-        sweep([&](uint32_t k, uint32_t, uint32_t, uint32_t, bool in) {
-            if (pass == 0 && !a.accumulate && in && k < a.V) atomicOr(a.named + (k >> 5), 1u << (k & 31));
-        });
+        sweep([](uint32_t, uint32_t, uint32_t, uint32_t, bool) {});
         __syncthreads();
         if (tid < bins) total[tid] = scan_warps(hist, tid);
         cluster_barrier();
@@ -477,74 +470,74 @@ __device__ void sort_swept(const GradArgs &a, uint32_t *smem) {
     }
 }
 
-// no row is named yet; the sort's first pass marks the rows
-template <bool kCluster>
-__device__ __forceinline__ void clear_named(const GradArgs &a) {
-    if (a.accumulate) return;
-    const int64_t first = (kCluster ? int64_t(cluster_rank()) * kSortThreads : 0) + threadIdx.x;
-    for (int64_t i = first; i < (a.V + 31) / 32; i += (kCluster ? kSortCtas : 1) * kSortThreads) __stcg(a.named + i, 0u);
-    if (kCluster) cluster_barrier();
-    else __syncthreads();
+__global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads) embed_mark_kernel(const GradArgs a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t first = int64_t(cluster_rank()) * kSortThreads + threadIdx.x, step = kSortCtas * kSortThreads;
+    for (int64_t i = first; i < (a.V + 31) / 32; i += step) __stcg(a.named + i, 0u);
+    cluster_barrier();
+#pragma unroll 4
+    for (int64_t t = first; t < a.T; t += step) {
+        const int64_t id = id_at(a.ids, t);
+        if (id >= 0 && id < a.V && id != a.pad) atomicOr(a.named + (id >> 5), 1u << (id & 31));
+    }
 }
 template <int kRounds>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_one_kernel(const GradArgs a, int rounds) {
     extern __shared__ uint32_t sort_smem[];
+    pdl_wait();                 // before the release: what starts after this kernel may rely on ids and marks
     pdl_launch_dependents();
-    pdl_wait();
-    clear_named<false>(a);
     sort_held<false, kRounds>(a, sort_smem, rounds);
 }
 template <int kRounds>
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort_held_kernel(const GradArgs a, int rounds) {
     extern __shared__ uint32_t sort_smem[];
+    pdl_wait();                 // before the release: what starts after this kernel may rely on ids and marks
     pdl_launch_dependents();
-    pdl_wait();
-    clear_named<true>(a);
     sort_held<true, kRounds>(a, sort_smem, rounds);
 }
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort_swept_kernel(const GradArgs a) {
     extern __shared__ uint32_t sort_smem[];
+    pdl_wait();                 // before the release: what starts after this kernel may rely on ids and marks
     pdl_launch_dependents();
-    pdl_wait();
-    clear_named<true>(a);
     sort_swept(a, sort_smem);
 }
 
-// Zero: a CTA of 256 threads for about 16 KB of rows, in the order of the table.  (A grid of two CTAs per SM
+// Zero: a CTA of 256 threads for up to 16 KB of rows, in the order of the table.  (A grid of two CTAs per SM
 // that strides over the rows wrote 6.0 TB/s, this order 7.2: what is written at any time lies close together.)
 constexpr int kZeroThreads = 256;
+constexpr int kZeroBytes = 16384;
+constexpr int kZeroWords = kZeroBytes / 16 / 32 + 1;      // words of bits of a CTA's rows, at 16 bytes a row
 template <bool kFew>
 __global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(const GradArgs a) {
-    __shared__ uint32_t s_named[kFew ? 32 : 1];
+    __shared__ uint32_t s_named[kZeroWords];
     pdl_launch_dependents();
-    if (a.T == 0) pdl_wait();   // otherwise the kernel before has let this one start, after its own wait for ids and sort
+    if (a.T == 0) pdl_wait();   // otherwise the kernels before have let this one start, after a wait for ids and marks
     const int64_t row_words = a.H * (a.de_bf16 ? 2 : 4) / 16;
-    const int64_t r0 = blockIdx.x * int64_t(a.zero_rows), end = min(r0 + a.zero_rows, a.V);
-    if (kFew) {                 // no sort has marked the rows: the CTA looks for its own among the few ids
-        if (threadIdx.x < 32) s_named[threadIdx.x] = 0;
-        __syncthreads();
+    const int64_t r0 = blockIdx.x * int64_t(a.zero_rows), end = min(r0 + a.zero_rows, a.V), b0 = r0 >> 5;
+    const int words = static_cast<int>(((end - 1) >> 5) - b0) + 1;
+    for (int i = threadIdx.x; i < words; i += kZeroThreads) s_named[i] = kFew || a.T == 0 ? 0u : __ldcg(a.named + b0 + i);
+    __syncthreads();
+    if (kFew) {                 // no marks: the CTA looks for its own rows among the few ids
         for (int t = threadIdx.x; t < a.T; t += kZeroThreads) {
             const int64_t id = id_at(a.ids, t);
-            if (id >= r0 && id < end && id != a.pad) atomicOr(s_named + ((id - r0) >> 5), 1u << ((id - r0) & 31));
+            if (id >= r0 && id < end && id != a.pad) atomicOr(s_named + ((id >> 5) - b0), 1u << (id & 31));
         }
         __syncthreads();
     }
-    auto named = [&](int64_t r) {
-        if (kFew) return (s_named[(r - r0) >> 5] >> ((r - r0) & 31)) & 1u;
-        return a.T > 0 ? (__ldcg(a.named + (r >> 5)) >> (r & 31)) & 1u : 0u;
-    };
+    auto named = [&](int64_t r) { return (s_named[(r >> 5) - b0] >> (r & 31)) & 1u; };
+    uint4 *dst = static_cast<uint4 *>(a.dE) + r0 * row_words;
     if (row_words >= kZeroThreads) {
-        for (int64_t r = r0; r < end; ++r) {
+        for (int64_t r = r0; r < end; ++r, dst += row_words) {
             if (named(r)) continue;
-            uint4 *dst = static_cast<uint4 *>(a.dE) + r * row_words;
 #pragma unroll 4
             for (int64_t i = threadIdx.x; i < row_words; i += kZeroThreads) dst[i] = make_uint4(0, 0, 0, 0);
         }
     } else {
-        // short rows: the CTA's words as one run (at most 1024, or one row's)
-        const uint32_t words = static_cast<uint32_t>((end - r0) * row_words), rw = static_cast<uint32_t>(row_words);
-        uint4 *dst = static_cast<uint4 *>(a.dE) + r0 * row_words;
-        for (uint32_t i = threadIdx.x; i < words; i += kZeroThreads)
+        // short rows: the CTA's words (at most 1024) as one run
+        const uint32_t all = static_cast<uint32_t>((end - r0) * row_words), rw = static_cast<uint32_t>(row_words);
+#pragma unroll 4
+        for (uint32_t i = threadIdx.x; i < all; i += kZeroThreads)
             if (!named(r0 + i / rw)) dst[i] = make_uint4(0, 0, 0, 0);
     }
     if (blockIdx.x == gridDim.x - 1) pdl_wait();
@@ -608,8 +601,8 @@ constexpr int kBatch = 4;
 template <bool kDyBf16, bool kDeBf16, bool kAdd>
 __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArgs a) {
     __shared__ uint32_t s_id[kMaxChunk + 2], s_pos[kMaxChunk];   // s_id[0]: the token before the chunk; last + 1: after it
-    pdl_wait();                 // before the release: `zero` may rely on the sort
     pdl_launch_dependents();
+    pdl_wait();
     const uint32_t *ids = a.key[a.passes & 1], *pos = a.pos[a.passes & 1];
     const int64_t ch = blockIdx.x;
     const int64_t i0 = ch * a.chunk;
@@ -663,8 +656,9 @@ __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArg
 
 // A few tokens (up to kFewTokens): one launch instead of sort, reduce and join.  Every block ranks the ids for
 // itself (a thread counts the smaller ones), and a group of blocks takes the ids that start in kFewRun
-// places of the sorted list, each to its end.
-constexpr int kFewTokens = kRedThreads;
+// places of the sorted list, each to its end.  Sorted / in one launch, rows of 4096 added: 9.2 / 3.4 us at 64
+// tokens, 9.3 / 4.3 at 128, 9.6 / 7.9 at 192, 9.9 / 9.8 at 256, 11.9 / 20.5 at 384 (the ranks grow with T^2).
+constexpr int kFewTokens = 192;
 constexpr int kFewRun = 4;
 template <bool kDyBf16, bool kDeBf16, bool kAdd>
 __global__ void __launch_bounds__(kRedThreads) embed_few_kernel(const GradArgs a) {
@@ -673,15 +667,16 @@ __global__ void __launch_bounds__(kRedThreads) embed_few_kernel(const GradArgs a
     pdl_launch_dependents();
     const int tid = threadIdx.x, T = static_cast<int>(a.T);
     const uint32_t V = static_cast<uint32_t>(a.V);
-    const uint32_t key = tid < T ? key_of(a, tid) : V;
-    s_key[tid] = key;
+    for (int t = tid; t < T; t += kRedThreads) s_key[t] = key_of(a, t);
     if (tid == 0) s_id[0] = s_id[T + 1] = 0xFFFFFFFFu;
     __syncthreads();
-    if (tid < T) {
+    for (int t = tid; t < T; t += kRedThreads) {
+        const uint32_t key = s_key[t];
         int place = 0;
-        for (int s = 0; s < T; ++s) place += s_key[s] < key || (s_key[s] == key && s < tid);
+#pragma unroll 8
+        for (int s = 0; s < T; ++s) place += s_key[s] < key || (s_key[s] == key && s < t);
         s_id[place + 1] = key;
-        s_pos[place] = tid;
+        s_pos[place] = t;
     }
     __syncthreads();
     int lo = blockIdx.x * kFewRun, hi = min(lo + kFewRun, T);

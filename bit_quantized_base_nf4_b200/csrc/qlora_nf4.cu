@@ -1124,6 +1124,8 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
         QL_TRY(launch_pdl("embed_few_kernel launch", sum[variant],
                           dim3(static_cast<unsigned>(ceil_div(T, emb::kFewRun)), static_cast<unsigned>(tiles)), emb::kRedThreads, 0, st, a));
     } else if (T > 0) {
+        if (!accumulate)
+            QL_TRY(launch_pdl("embed_mark_kernel launch", emb::embed_mark_kernel, dim3(emb::kSortCtas), emb::kSortThreads, 0, st, a));
         if (T <= emb::kHeldTokens) {
             const bool one = T <= emb::kOneTokens;
             const int rounds = static_cast<int>(ceil_div(T, int64_t(one ? 1 : emb::kSortCtas) * emb::kSortThreads));
@@ -1152,8 +1154,7 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
                           emb::kJoinWarps * 32, 0, st, a));
     }
     if (!accumulate) {
-        // rows of about 16 KB a CTA
-        a.zero_rows = static_cast<int>(std::min<int64_t>(V, std::max<int64_t>(1, 16384 / (H * (de_is_bf16 ? 2 : 4)))));
+        a.zero_rows = static_cast<int>(std::min<int64_t>(V, std::max<int64_t>(1, emb::kZeroBytes / (H * (de_is_bf16 ? 2 : 4)))));
         QL_TRY(launch_pdl("embed_zero_kernel launch", few ? emb::embed_zero_kernel<true> : emb::embed_zero_kernel<false>,
                           dim3(static_cast<unsigned>(ceil_div(V, a.zero_rows))), emb::kZeroThreads, 0, st, a));
     }

@@ -158,6 +158,9 @@ GRAD = [
     (128, 40, 1160, "zipf", torch.bfloat16, torch.float32, False, 2, 1.0, torch.int64),
     (128, 4096, 24, "one", torch.float32, torch.bfloat16, True, -1, 0.5, torch.int32),
     (129, 40, 1160, "zipf", torch.bfloat16, torch.float32, False, 2, 1.0, torch.int64),
+    (192, 700, 1160, "zipf", torch.bfloat16, torch.float32, True, 2, 1.0, torch.int64),
+    (192, 9, 64, "runs", torch.float32, torch.float32, False, -1, 1.0, torch.int32),
+    (193, 700, 1160, "zipf", torch.bfloat16, torch.float32, False, 2, 1.0, torch.int64),
     (101, 30_000, 4096, "any", torch.bfloat16, torch.float32, False, 0, 1.0, torch.int64),
     (77, 3, 520, "runs", torch.bfloat16, torch.bfloat16, False, -1, 1.0, torch.int32),
     (1000, 513, 264, "zipf", torch.bfloat16, torch.float32, False, 0, 1.0, torch.int32),
