@@ -55,6 +55,37 @@ struct alignas(256) PlanHead {
     double partial[kPartials];
 };
 
+// A tensor of a plan as the host hands it over: its first chunk (n not set), where its chunks begin in the list,
+// and the bytes of an element of p, g and the states.
+struct TensorDesc {
+    Chunk base;
+    int64_t numel, first;
+    int32_t pb, gb, sb, unused;
+};
+// Writes the chunk list: a thread a chunk, which finds its tensor by the first chunk of each (ascending).
+__global__ void __launch_bounds__(kThreads) expand_plan_kernel(const TensorDesc *ts, int count, int chunk, int64_t nchunks, Chunk *out) {
+    const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+    if (i >= nchunks) return;
+    int lo = 0, hi = count;                       // ts[lo].first <= i < ts[hi].first
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (ts[mid].first <= i) lo = mid;
+        else hi = mid;
+    }
+    const TensorDesc &t = ts[lo];
+    const int64_t e = (i - t.first) * chunk;
+    Chunk c = t.base;
+    c.n = static_cast<int32_t>(min(int64_t(chunk), t.numel - e));
+    c.g += uint64_t(e) * t.gb;
+    if (c.p) c.p += uint64_t(e) * t.pb;
+    if (c.copy) c.copy += uint64_t(e) * 2;
+    if (c.m) c.m += uint64_t(e) * t.sb;
+    if (c.v) c.v += uint64_t(e) * t.sb;
+    if (c.dm) c.dm += uint64_t(e / kBlock) * 4;
+    if (c.dv) c.dv += uint64_t(e / kBlock) * 4;
+    out[i] = c;
+}
+
 __device__ __forceinline__ uint32_t chunk_word(const Chunk *chunks, int64_t c, int lane) {
     return lane < 20 ? __ldg(reinterpret_cast<const uint32_t *>(chunks + c) + lane) : 0u;
 }

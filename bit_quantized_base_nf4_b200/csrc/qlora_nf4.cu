@@ -1258,10 +1258,15 @@ static int64_t plan_chunks(const qlora_adamw_tensor *ts, int64_t count, int64_t 
     return n;
 }
 
+// head, chunk list, tensors
+static size_t plan_need(int64_t count, int64_t nchunks) {
+    return sizeof(optim::PlanHead) + size_t(nchunks) * sizeof(optim::Chunk) + size_t(count) * sizeof(optim::TensorDesc);
+}
+
 size_t qlora_adamw_plan_bytes(const qlora_adamw_tensor *tensors, int64_t count) {
     int64_t numel = 0;
     if (check_opt_tensors(tensors, count, &numel) != QLORA_OK) return 0;
-    return sizeof(optim::PlanHead) + size_t(plan_chunks(tensors, count, plan_chunk(numel))) * sizeof(optim::Chunk);
+    return plan_need(count, plan_chunks(tensors, count, plan_chunk(numel)));
 }
 
 qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t count, void *buffer, size_t bytes,
@@ -1273,7 +1278,7 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     QL_TRY(check_opt_overlap(tensors, count));
     const int64_t chunk = plan_chunk(numel), nchunks = plan_chunks(tensors, count, chunk);
     if (nchunks > (1 << 30)) return fail(QLORA_ERR_SHAPE, "the tensors have too many elements for one plan");
-    const size_t need = sizeof(optim::PlanHead) + size_t(nchunks) * sizeof(optim::Chunk);
+    const size_t need = plan_need(count, nchunks);
     if (!buffer || bytes < need) return fail(QLORA_ERR_WORKSPACE, "the plan buffer holds %zu bytes, %zu needed", buffer ? bytes : size_t(0), need);
     if (reinterpret_cast<uintptr_t>(buffer) % 256) return fail(QLORA_ERR_ALIGN, "the plan buffer must be 256-byte aligned");
     QL_TRY(require_sm100());
@@ -1281,42 +1286,54 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     QL_TRY(cuda_check(cudaStreamIsCapturing(st, &cap), "cudaStreamIsCapturing"));
     if (cap != cudaStreamCaptureStatusNone) return fail(QLORA_ERR_ARG, "a plan cannot be made during stream capture");
-    uint8_t *host = static_cast<uint8_t *>(std::calloc(1, need));
-    if (!host) return fail(QLORA_ERR_ARG, "no host memory for the plan (%zu bytes)", need);
-    // chunks of tensors with 32-bit states first, then those with 8-bit states: a kernel for each
-    optim::Chunk *const list = reinterpret_cast<optim::Chunk *>(host + sizeof(optim::PlanHead)), *c = list;
-    int64_t chunks32 = 0;
+    optim::TensorDesc *const host = static_cast<optim::TensorDesc *>(std::calloc(size_t(count), sizeof(optim::TensorDesc)));
+    if (!host) return fail(QLORA_ERR_ARG, "no host memory for the plan");
+    // tensors with 32-bit states first, then those with 8-bit states: a kernel for each
+    int64_t n = 0, first = 0, chunks32 = 0;
     int32_t grad_only = 0, elem8 = 0;
     for (int pass = 0; pass < 2; ++pass) {
         for (int64_t i = 0; i < count; ++i) {
             const qlora_adamw_tensor &t = tensors[i];
             const bool only = (t.flags & QLORA_OPT_GRAD_ONLY) != 0, eight = !only && (t.flags & QLORA_OPT_STATE_8BIT) != 0;
-            if (eight != (pass == 1)) continue;
-            if (only && t.numel) grad_only = 1;
-            const int64_t pb = (t.flags & QLORA_OPT_PARAM_BF16) ? 2 : 4, gb = (t.flags & QLORA_OPT_GRAD_BF16) ? 2 : 4, sb = eight ? 1 : 4;
-            auto at = [](const void *base, int64_t off) { return base ? uint64_t(reinterpret_cast<uintptr_t>(base)) + uint64_t(off) : 0; };
-            if (eight && t.numel) elem8 = std::max(elem8, static_cast<int32_t>(gb + pb + 2));
-            for (int64_t e = 0; e < t.numel; e += chunk, ++c) {
-                c->g = at(t.grad, e * gb);
-                c->n = static_cast<int32_t>(std::min(chunk, t.numel - e));
-                c->flags = uint32_t(t.flags) & (optim::kParamBf16 | optim::kGradBf16);
-                if (only) continue;
-                c->p = at(t.param, e * pb);
-                c->copy = at(t.param_bf16, e * 2);
-                c->m = at(t.exp_avg, e * sb);
-                c->v = at(t.exp_avg_sq, e * sb);
-                c->dm = eight ? at(t.exp_avg_step, e / optim::kBlock * 4) : 0;
-                c->dv = eight ? at(t.exp_avg_sq_step, e / optim::kBlock * 4) : 0;
-                c->lr_scale = t.lr_scale;
-                c->decay = t.weight_decay;
+            if (t.numel == 0 || eight != (pass == 1)) continue;
+            auto at = [](const void *p) { return uint64_t(reinterpret_cast<uintptr_t>(p)); };
+            optim::TensorDesc &d = host[n++];
+            d.numel = t.numel;
+            d.first = first;
+            first += ceil_div(t.numel, chunk);
+            d.pb = (t.flags & QLORA_OPT_PARAM_BF16) ? 2 : 4;
+            d.gb = (t.flags & QLORA_OPT_GRAD_BF16) ? 2 : 4;
+            d.sb = eight ? 1 : 4;
+            d.base.g = at(t.grad);
+            d.base.flags = uint32_t(t.flags) & (optim::kParamBf16 | optim::kGradBf16);
+            if (only) {
+                grad_only = 1;
+                continue;
             }
+            d.base.p = at(t.param);
+            d.base.copy = at(t.param_bf16);
+            d.base.m = at(t.exp_avg);
+            d.base.v = at(t.exp_avg_sq);
+            d.base.dm = eight ? at(t.exp_avg_step) : 0;
+            d.base.dv = eight ? at(t.exp_avg_sq_step) : 0;
+            d.base.lr_scale = t.lr_scale;
+            d.base.decay = t.weight_decay;
+            if (eight) elem8 = std::max(elem8, d.gb + d.pb + 2);
         }
-        if (pass == 0) chunks32 = c - list;
+        if (pass == 0) chunks32 = first;
     }
-    cudaError_t e = cudaMemcpyAsync(buffer, host, need, cudaMemcpyHostToDevice, st);
+    optim::Chunk *const list = reinterpret_cast<optim::Chunk *>(static_cast<optim::PlanHead *>(buffer) + 1);
+    optim::TensorDesc *const descs = reinterpret_cast<optim::TensorDesc *>(list + nchunks);
+    cudaError_t e = cudaMemsetAsync(buffer, 0, sizeof(optim::PlanHead), st);
+    if (e == cudaSuccess && n > 0) e = cudaMemcpyAsync(descs, host, size_t(n) * sizeof(optim::TensorDesc), cudaMemcpyHostToDevice, st);
+    if (e == cudaSuccess && n > 0) {
+        optim::expand_plan_kernel<<<static_cast<unsigned>(ceil_div(nchunks, optim::kThreads)), optim::kThreads, 0, st>>>(
+            descs, static_cast<int>(n), static_cast<int>(chunk), nchunks, list);
+        e = cudaGetLastError();
+    }
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
     std::free(host);
-    QL_TRY(cuda_check(e, "copy of the plan"));
+    QL_TRY(cuda_check(e, "making of the plan"));
     plan->buffer = buffer;
     plan->chunks = nchunks;
     plan->chunks32 = chunks32;

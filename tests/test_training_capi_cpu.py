@@ -109,9 +109,9 @@ def test_plan_bytes_count_chunks(lib):
     head = f((_capi.AdamWTensorC * 1)(_tensor(numel=0)), 1)
     assert f((_capi.AdamWTensorC * 1)(_tensor(numel=1)), 1) == head + 80
     assert f((_capi.AdamWTensorC * 1)(_tensor(numel=257)), 1) == head + 160
-    # a large plan takes chunks of 1024
-    n = 64 * 148 * 1024
-    assert f((_capi.AdamWTensorC * 2)(_tensor(numel=n), _tensor(numel=1025)), 2) == head + (n // 1024 + 2) * 80
+    # a large plan takes chunks of 1024; each tensor costs the same besides
+    n, one = 64 * 148 * 1024, f((_capi.AdamWTensorC * 2)(_tensor(numel=0), _tensor(numel=0)), 2) - head
+    assert f((_capi.AdamWTensorC * 2)(_tensor(numel=n), _tensor(numel=1025)), 2) == head + one + (n // 1024 + 2) * 80
     assert f(None, 1) == 0 and f((_capi.AdamWTensorC * 1)(_tensor()), 0) == 0
 
 
