@@ -309,8 +309,9 @@ qlora_status qlora_embed_fwd(const void *E, int e_is_bf16, int64_t V, int64_t H,
  * accumulate: the float32 sum of the old value and the scaled sum).  Tokens with
  * id padding_id take no part (-1: none does).  The tokens are sorted by id, so
  * equal ids add up in an order fixed by the ids: results repeat bit for bit.
- * ws / ws_bytes: caller scratch of qlora_embed_grad_workspace_bytes(T, V, H); two
- * calls whose work overlaps in time need a scratch each. */
+ * dE must not overlap dY, ids or ws.  ws / ws_bytes: caller scratch of
+ * qlora_embed_grad_workspace_bytes(T, V, H); two calls whose work overlaps in time
+ * need a scratch each. */
 size_t qlora_embed_grad_workspace_bytes(int64_t T, int64_t V, int64_t H);
 qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const void *dY, int dy_is_bf16, int64_t V,
                               int64_t H, float scale, int64_t padding_id, void *dE, int de_is_bf16, int accumulate,

@@ -172,6 +172,8 @@ GRAD = [
     (70_001, 262_144, 16, "zipf", torch.float32, torch.float32, False, -1, 1.0, torch.int32),
     (131_072, 50_000, 8, "zipf", torch.float32, torch.float32, False, -1, 1.0, torch.int64),
     (131_073, 50_000, 8, "zipf", torch.float32, torch.float32, False, -1, 1.0, torch.int64),
+    (152_000, 50, 8, "zipf", torch.bfloat16, torch.float32, False, -1, 1.0, torch.int64),       # chunks of 128, swept sort
+    (76_000, 900, 1032, "zipf", torch.bfloat16, torch.bfloat16, True, 4, 1.0, torch.int32),      # chunks of 128, held sort
     (200_003, 300_000, 24, "any", torch.bfloat16, torch.float32, True, 5, 1.0, torch.int32),
 ]
 
