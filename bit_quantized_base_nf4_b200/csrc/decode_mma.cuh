@@ -106,6 +106,8 @@ __device__ __forceinline__ uint32_t lut_at(uint32_t lut_lane, uint32_t w, int c)
     asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(lut_lane + (e << 7)));
     return v;
 }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // global -> shared bulk copy (16-byte aligned addresses, size a multiple of 16)
 __device__ __forceinline__ void bulk_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(

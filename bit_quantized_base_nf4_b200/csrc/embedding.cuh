@@ -9,6 +9,7 @@
 #include "ptx.cuh"
 #include "quant_kernels.cuh"
 #include "scale_src.cuh"
+#include "step_common.cuh"
 
 namespace qlora {
 namespace emb {

@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include "ptx.cuh"
+#include "step_common.cuh"
 
 namespace qlora {
 namespace optim {
