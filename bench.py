@@ -40,10 +40,10 @@ CSRC = os.path.join(ROOT, "bit_quantized_base_nf4_b200", "csrc")
 # hash of the kernel sources that capture ran; a source change makes the figure stale
 # and the bench then reports null
 KERNEL_TRAFFIC = {
-    # attention 162.1 + 46.2 MB, FFN up 852.0 + 57.9 MB, FFN down 847.1 + 211.6 MB
-    "dx": {"bytes": 2176886272, "src_sha": "8d831963ce15634a"},
-    # attention 111.4 + 51.2 MB, FFN up 1952.1 + 222.3 MB, FFN down 1168.5 + 58.7 MB
-    "fwd": {"bytes": 3564198400, "src_sha": "08e3f1cc905141cf"},
+    # attention 167.3 + 46.2 MB, FFN up 852.3 + 59.1 MB, FFN down 890.2 + 210.8 MB
+    "dx": {"bytes": 2225984256, "src_sha": "7c5f1f442424223a"},
+    # attention 123.8 + 50.6 MB, FFN up 1853.1 + 222.7 MB, FFN down 1170.4 + 58.7 MB
+    "fwd": {"bytes": 3479323392, "src_sha": "64cd4c072b726fb1"},
 }
 
 
