@@ -426,6 +426,9 @@ qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double be
     if (plan->grad_only) return fail(QLORA_ERR_ARG, "the plan holds QLORA_OPT_GRAD_ONLY tensors");
     if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1)) return fail(QLORA_ERR_ARG, "betas must be in [0, 1)");
     if (!(eps >= 0) || !std::isfinite(eps)) return fail(QLORA_ERR_ARG, "eps must be finite and not negative");
+    // a smaller eps (1 - beta1^t), the denominator of an element that never had a gradient, would count as zero
+    if (eps > 0 && eps * (1.0 - beta1) < 1.17549435082228751e-38)
+        return fail(QLORA_ERR_ARG, "eps must be 0, or eps (1 - beta1) at least 2^-126");
     if (!lr_dev && !(lr >= 0 && std::isfinite(lr))) return fail(QLORA_ERR_ARG, "lr must be finite and not negative");
     if (step_dev ? step != 0 : step < 1)
         return fail(QLORA_ERR_ARG, "step (%lld) must be at least 1, or 0 with a step counter on the device", (long long)step);

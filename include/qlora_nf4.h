@@ -393,7 +393,8 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
  *   grad_scale: device float32, the clip coefficient (out + 1 of qlora_grad_norm),
  *     or NULL.  A value that is not finite makes the step change nothing (the
  *     counter included).
- * 0 <= beta < 1, eps >= 0, lr >= 0.  The plan buffer holds scratch: two calls on
+ * 0 <= beta < 1, lr >= 0, and eps = 0 or eps (1 - beta1) >= 2^-126 (with eps = 0 an
+ * element whose v is zero becomes NaN or infinite, as in the formula).  The plan buffer holds scratch: two calls on
  * one plan whose work overlaps in time race. */
 qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double beta1, double beta2, double eps,
                               int64_t step, const float *grad_scale, const float *lr_dev, int64_t *step_dev,

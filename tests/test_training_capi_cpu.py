@@ -206,3 +206,15 @@ def test_norm_and_adam8_refusals(lib):
         assert f(*args(0, 0x1008, 0x2000, 0x3000, 10)) == ALIGN
         assert f(*args(1, 0x1000, 0x2002, 0x3000, 10)) == ALIGN
         assert f(*args(1, None, None, None, 0)) == 0
+
+
+@pytest.mark.parametrize("b1,eps", [(0.9, 1e-39), (0.9, 1e-45), (0.9, 1e-300), (0.9, 1.1e-37), (1 - 1e-10, 1e-30)])
+def test_step_refuses_an_eps_that_would_count_as_zero(lib, b1, eps):
+    assert _step(lib, b1=b1, eps=eps) == ARG and "2^-126" in _err(lib)
+    assert _step(lib, b1=b1, eps=eps, step=0, sd=0x9000) == ARG and "2^-126" in _err(lib)
+
+
+@pytest.mark.parametrize("b1,eps", [(0.9, 0.0), (0.9, 1.2e-37), (0.0, 1.2e-38)])
+def test_step_takes_the_smallest_eps(lib, b1, eps):
+    # refused for its step number only, which is looked at after eps
+    assert _step(lib, b1=b1, eps=eps, step=-1) == ARG and "step (-1)" in _err(lib)
