@@ -431,6 +431,8 @@ class AdamWTensor:
                    *(torch.zeros((n + 255) // 256, dtype=torch.float32, device=dev) for _ in range(2)), **kw)
 
     def c_struct(self) -> _capi.AdamWTensorC:
+        if self.grad is None:
+            raise ValueError("grad is required")
         dev, n = torch.cuda.current_device(), self.grad.numel()
         flags = _capi.OPT_GRAD_BF16 if _flat(self.grad, n, dev, _FLOATS, "grad") is torch.bfloat16 else 0
         if self.param is None:

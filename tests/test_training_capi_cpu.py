@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from bit_quantized_base_nf4_b200 import _capi
+from bit_quantized_base_nf4_b200 import AdamWTensor, _capi
 from bit_quantized_base_nf4_b200 import build as libbuild
 
 P = ctypes.c_void_p
@@ -218,3 +218,8 @@ def test_step_refuses_an_eps_that_would_count_as_zero(lib, b1, eps):
 def test_step_takes_the_smallest_eps(lib, b1, eps):
     # refused for its step number only, which is looked at after eps
     assert _step(lib, b1=b1, eps=eps, step=-1) == ARG and "step (-1)" in _err(lib)
+
+
+def test_a_tensor_without_a_gradient_is_named():
+    with pytest.raises(ValueError, match="grad is required"):
+        AdamWTensor(None, None).c_struct()
