@@ -476,7 +476,8 @@ def _flat(t, n: int, dev: int, dtypes, name: str):
 @dataclass
 class AdamWPlan:
     """A list of tensors prepared for qlora_adamw_step and qlora_grad_norm; keeps the tensors and the device
-    buffer alive.  Made by qlora_adamw_plan_init."""
+    buffer alive.  Made by qlora_adamw_plan_init, whose stream the buffer belongs to: a plan that is used on
+    another stream has to live until that work is done, like the tensors it names."""
     tensors: list
     buffer: torch.Tensor
     c_plan: _capi.AdamWPlanC
@@ -489,7 +490,9 @@ def qlora_adamw_plan_init(tensors, stream=None) -> AdamWPlan:
     dev = torch.cuda.current_device()
     arr = (_capi.AdamWTensorC * len(tensors))(*(t.c_struct() for t in tensors))
     nbytes = _lib().qlora_adamw_plan_bytes(arr, len(tensors))
-    buffer = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device="cuda")
+    # from the pool of the stream that fills it: a block of the current stream's pool may still be written there
+    with torch.cuda.stream(stream):
+        buffer = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device="cuda")
     plan = AdamWPlan(tensors, buffer, _capi.AdamWPlanC())
     _capi.check("qlora_adamw_plan_init", _lib().qlora_adamw_plan_init(arr, len(tensors), buffer.data_ptr(), buffer.numel(),
                                                                       ctypes.byref(plan.c_plan), _raw_stream(stream, dev)))

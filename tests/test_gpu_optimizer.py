@@ -288,6 +288,30 @@ def test_step_on_another_stream():
     mo.check("side stream")
 
 
+def test_plan_made_on_another_stream_while_the_current_one_writes_freed_memory():
+    # a freed block of the current stream's pool goes to the next request there, with its writes still queued
+    g = torch.Generator().manual_seed(17)
+    t = _make(g, 3000, torch.float32, torch.float32, 32, False)
+    plain, side = q.qlora_adamw_plan_init([t]), torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        busy @ busy
+    old = [torch.empty_like(plain.buffer).fill_(0xAB) for _ in range(8)]
+    del old
+    plan = q.qlora_adamw_plan_init([t], stream=side)
+    torch.cuda.synchronize()
+    # behind the head (scratch): chunks and tensors; nothing is launched on a list that differs
+    used = plan.c_plan.chunks * 80
+    head = 256 + 8 * 4096
+    assert torch.equal(plan.buffer[head:head + used], plain.buffer[head:head + used])
+    mo = Model(t)
+    q.qlora_adamw_step(plan, 1e-3, 1, stream=side)
+    q.qlora_sync_status(side)
+    mo.step(1, 1e-3, None)
+    mo.check("plan of a side stream")
+
+
 # ----------------------------------------------------------------- the norm
 
 @pytest.mark.parametrize("sizes", [[1], [255, 0, 257], [4097, 100_003, 1, 64], [64 * 148 * 2048 + 77]])
