@@ -249,6 +249,7 @@ static qlora_status check_opt_tensors(const qlora_adamw_tensor *ts, int64_t coun
         if (t.flags & ~kOptFlags) return fail(QLORA_ERR_ARG, "tensor %lld: unknown flags (%d)", k, t.flags);
         if (t.numel == 0) continue;
         *numel += t.numel;
+        if (*numel > (int64_t(1) << 40)) return fail(QLORA_ERR_SHAPE, "the tensors have too many elements for one plan (tensor %lld)", k);
         if (!t.grad) return fail(QLORA_ERR_ARG, "tensor %lld: grad is NULL", k);
         if (!aligned16(t.grad)) return fail(QLORA_ERR_ALIGN, "tensor %lld: grad must be 16-byte aligned", k);
         if (t.flags & QLORA_OPT_GRAD_ONLY) continue;

@@ -68,3 +68,25 @@ def test_no_second_level_scales_without_double_quantization(lib):
     assert lib.qlora_dequant(ctypes.byref(w), P(0x20008), 0, None) == ALIGN and "out must" in _err(lib)
     w.format = 0
     assert lib.qlora_dequant(ctypes.byref(w), P(0x20008), 0, None) == ARG
+
+
+def _huge(at):
+    """A tensor of 2^40 elements whose buffers lie far apart."""
+    return _tensor(numel=1 << 40, **{k: at + (i << 50) for i, k in enumerate(("param", "grad", "exp_avg", "exp_avg_sq"), 1)})
+
+
+@pytest.mark.parametrize("tensors", [
+    [_huge(0), _huge(1 << 60)],                   # more elements than a plan takes
+])
+def test_plan_bytes_are_zero_for_a_list_that_plan_init_refuses(lib, tensors):
+    arr, plan = (_capi.AdamWTensorC * len(tensors))(*tensors), _capi.AdamWPlanC()
+    assert lib.qlora_adamw_plan_init(arr, len(tensors), P(0x1000000), 1 << 62, ctypes.byref(plan), None) in (ARG, SHAPE)
+    assert lib.qlora_adamw_plan_bytes(arr, len(tensors)) == 0
+
+
+def test_a_list_whose_elements_pass_64_bits_is_refused(lib):
+    # 2^23 tensors of 2^40 elements: the sum of the elements would wrap
+    n = 1 << 23
+    one = bytes(_tensor(numel=1 << 40, grad=0x20000, flags=8))               # gradients alone, which may share memory
+    arr = (_capi.AdamWTensorC * n).from_buffer(bytearray(one * n))
+    assert lib.qlora_adamw_plan_bytes(arr, n) == 0 and "too many elements" in _err(lib)
