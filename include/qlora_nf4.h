@@ -374,7 +374,8 @@ typedef struct {
 } qlora_adamw_plan;
 
 /* Bytes of the plan buffer for these tensors (host arithmetic only); 0 for a list
- * that qlora_adamw_plan_init would refuse. */
+ * with a tensor that qlora_adamw_plan_init would refuse by itself, or of more than
+ * 2^40 elements in all.  Overlaps are looked at by qlora_adamw_plan_init alone. */
 size_t qlora_adamw_plan_bytes(const qlora_adamw_tensor *tensors, int64_t count);
 
 /* Fills *plan (host) and `buffer` (device, 256-byte aligned, `bytes` of at least

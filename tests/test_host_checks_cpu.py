@@ -90,3 +90,12 @@ def test_a_list_whose_elements_pass_64_bits_is_refused(lib):
     one = bytes(_tensor(numel=1 << 40, grad=0x20000, flags=8))               # gradients alone, which may share memory
     arr = (_capi.AdamWTensorC * n).from_buffer(bytearray(one * n))
     assert lib.qlora_adamw_plan_bytes(arr, n) == 0 and "too many elements" in _err(lib)
+
+
+@pytest.mark.parametrize("tensors", [[_tensor(), _tensor()], [_tensor(exp_avg_sq=0x30000)]])
+def test_overlaps_are_found_by_plan_init_alone(lib, tensors):
+    # as the header says: the bytes are those of the list, whatever its buffers do to one another
+    arr, plan = (_capi.AdamWTensorC * len(tensors))(*tensors), _capi.AdamWPlanC()
+    need = lib.qlora_adamw_plan_bytes(arr, len(tensors))
+    assert need > 0
+    assert lib.qlora_adamw_plan_init(arr, len(tensors), P(0x1000000), need, ctypes.byref(plan), None) == ARG and "overlaps" in _err(lib)
