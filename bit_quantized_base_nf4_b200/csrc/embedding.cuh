@@ -25,7 +25,8 @@ __device__ __forceinline__ int64_t id_at(const Ids &ids, int64_t t) {
     return ids.is64 ? __ldcg(reinterpret_cast<const long long *>(ids.ptr) + t)
                     : int64_t(__ldcg(reinterpret_cast<const int *>(ids.ptr) + t));
 }
-__device__ __forceinline__ void report_bad_id() { atomicExch(&g_device_error, kDeviceErrIndex); }
+// (only where nothing is recorded yet: a timeout or a failed tensor-memory store of an earlier kernel is the graver error)
+__device__ __forceinline__ void report_bad_id() { atomicCAS(&g_device_error, 0, kDeviceErrIndex); }
 
 // ------------------------------------------------------------------ lookup
 // y[t, :] = round(scale * w'[id_t, :]), w' the table's float32 values (4-bit: fp32(c[code] s_b);

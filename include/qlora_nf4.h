@@ -404,7 +404,7 @@ qlora_status qlora_adamw_step(const qlora_adamw_plan *plan, double lr, double be
 /* out[0] = the 2-norm of all gradients of the plan together, out[1] = the clip
  * coefficient min(1, max_norm / (norm + 1e-6)), NaN when the norm is not finite
  * (device float32[2]).  Squares are summed in float64, in an order fixed by the
- * plan.  max_norm > 0 (infinity: no limit).  Scratch as for qlora_adamw_step. */
+ * plan; a norm beyond float32's range gives out[0] = infinity and out[1] as above.  max_norm > 0 (infinity: no limit).  Scratch as for qlora_adamw_step. */
 qlora_status qlora_grad_norm(const qlora_adamw_plan *plan, float max_norm, float *out, void *stream);
 
 /* The 8-bit state from and as float32 (loading and writing checkpoints): x [numel]
@@ -417,7 +417,8 @@ qlora_status qlora_adam8_decode(const void *codes, int kind, const float *steps,
 /* Waits for `stream`, then reports and clears a device-side error recorded by
  * any earlier kernel of this library on the current device: a pipeline wait
  * that timed out (QLORA_ERR_TIMEOUT), a tensor-memory store whose read-back
- * check failed (QLORA_ERR_CUDA) or a token id outside its table (QLORA_ERR_ARG). */
+ * check failed (QLORA_ERR_CUDA) or a token id outside its table (QLORA_ERR_ARG).
+ * Of several, a token id is reported last. */
 qlora_status qlora_sync_status(void *stream);
 
 /* Message describing the last failure on the calling thread ("" if none). */
