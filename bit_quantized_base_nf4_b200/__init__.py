@@ -475,12 +475,16 @@ def _flat(t, n: int, dev: int, dtypes, name: str):
 
 @dataclass
 class AdamWPlan:
-    """A list of tensors prepared for qlora_adamw_step and qlora_grad_norm; keeps the tensors and the device
-    buffer alive.  Made by qlora_adamw_plan_init, whose stream the buffer belongs to: a plan that is used on
-    another stream has to live until that work is done, like the tensors it names."""
+    """A list of tensors prepared for qlora_adamw_step and qlora_grad_norm; keeps the buffers it names and the
+    device buffer alive.  The calls go to the addresses of the time it was made: a field of an AdamWTensor that is
+    assigned anew (a gradient that is allocated each step) does not change the plan, so fill the same buffers
+    or make another plan.  Made by qlora_adamw_plan_init, whose stream the buffer belongs to: a plan that is used on
+    another stream has to live until that work is done, like the tensors it names.  The buffer holds scratch of the
+    norm and of a counted step: calls on one plan must not overlap in time."""
     tensors: list
     buffer: torch.Tensor
     c_plan: _capi.AdamWPlanC
+    held: tuple = ()
 
 
 def qlora_adamw_plan_init(tensors, stream=None) -> AdamWPlan:
@@ -493,7 +497,8 @@ def qlora_adamw_plan_init(tensors, stream=None) -> AdamWPlan:
     # from the pool of the stream that fills it: a block of the current stream's pool may still be written there
     with torch.cuda.stream(stream):
         buffer = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device="cuda")
-    plan = AdamWPlan(tensors, buffer, _capi.AdamWPlanC())
+    held = tuple(x for t in tensors for x in vars(t).values() if isinstance(x, torch.Tensor))
+    plan = AdamWPlan(tensors, buffer, _capi.AdamWPlanC(), held)
     _capi.check("qlora_adamw_plan_init", _lib().qlora_adamw_plan_init(arr, len(tensors), buffer.data_ptr(), buffer.numel(),
                                                                       ctypes.byref(plan.c_plan), _raw_stream(stream, dev)))
     return plan

@@ -418,7 +418,7 @@ qlora_status qlora_adam8_decode(const void *codes, int kind, const float *steps,
  * any earlier kernel of this library on the current device: a pipeline wait
  * that timed out (QLORA_ERR_TIMEOUT), a tensor-memory store whose read-back
  * check failed (QLORA_ERR_CUDA) or a token id outside its table (QLORA_ERR_ARG).
- * Of several, a token id is reported last. */
+ * Of several one is reported, a token id only when there is no other. */
 qlora_status qlora_sync_status(void *stream);
 
 /* Message describing the last failure on the calling thread ("" if none). */

@@ -1,4 +1,7 @@
-"""What the training-step calls leave to their caller: which error is reported, the list of a plan."""
+"""What the training-step calls leave to their caller: which error is reported, what a plan keeps and lists."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -35,6 +38,25 @@ def test_a_bad_id_does_not_hide_a_timeout(order, call):
     bad_ids()
     with pytest.raises(q.QloraError, match="token id"):
         q.qlora_sync_status()
+
+
+def test_a_plan_keeps_its_buffers_when_a_field_is_assigned_anew():
+    t = q.AdamWTensor.zeros(torch.zeros(5000, device=DEV), torch.ones(5000, device=DEV), bits=8,
+                            param_bf16=torch.zeros(5000, dtype=torch.bfloat16, device=DEV))
+    plan = q.qlora_adamw_plan_init([t])
+    fields = ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_step", "exp_avg_sq_step", "param_bf16")
+    kept = {f: weakref.ref(getattr(t, f)) for f in fields}
+    for f in fields:
+        setattr(t, f, None)
+    gc.collect()
+    assert [f for f in fields if kept[f]() is None] == []
+    # and the plan still works on them
+    q.qlora_adamw_step(plan, 1e-3, 1)
+    q.qlora_sync_status()
+    assert torch.allclose(kept["param"](), torch.full((5000,), -1e-3, device=DEV), rtol=1e-5)
+    del plan
+    gc.collect()
+    assert [f for f in fields if kept[f]() is not None] == []
 
 
 def test_plans_made_on_two_streams_hold_the_same_list():
