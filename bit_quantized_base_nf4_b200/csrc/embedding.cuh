@@ -207,19 +207,20 @@ __global__ void __launch_bounds__(kFwdThreads) embed_fwd_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ gradient
-// dE[v, :] (+)= scale * sum over the tokens t with id_t = v of dY[t, :], in three or five launches:
-//   mark    (unless the gradient is added) sets a bit for every row that a token names;
+// dE[v, :] (+)= scale * sum over the tokens t with id_t = v of dY[t, :], in three or four launches:
+//   mark    (where the cluster sorts, and unless the gradient is added) sets a bit for every row that a token names;
 //   sort    the tokens by id (stable);
 //   reduce  equal runs of `chunk` sorted tokens each: an id that lies wholly in a chunk is summed
 //           and written, one that crosses a border leaves a partial sum per chunk;
-//   join    adds the partial sums of each such id in order and writes its row;
-//   zero    (unless the gradient is added) zeroes the rows without a bit.
-// Up to kFewTokens tokens take one launch in place of the first four, and `zero` looks at the ids itself.
+//   join    adds the partial sums of each such id in order and writes its row.
+// Unless the gradient is added, further CTAs of these launches zero the table: the whole of it beside the sort where that
+// takes one CTA, else the rows without a bit.
+// Up to kFewTokens tokens take one launch, whose zeroing CTAs look at the ids themselves.
 // Every sum is float32, in an order fixed by the ids alone: results repeat bit for bit.
-// Programmatic dependent launch: a kernel starts once the one before it has started, and the sort is let
-// start before it waits for the marks but lets the others start only then.  So `zero`, whose writes are nearly all of the time
-// when the table is large, needs no wait of its own and runs beside the sort and the reduction; its last
-// CTA waits for the join, so that its completion means the whole call's.
+// Programmatic dependent launch: a kernel may start while the one before it still runs, and every thread waits for
+// that one to end before it reads or writes global memory: the trigger of a launch promises no visibility, not even of
+// what was complete before it.  (So no launch of zeros runs beside the whole chain: 8192 x 4096 into 32000 rows takes
+// 114 us where one that relied on the trigger took 107, 2047 x 4096 takes 88 as it did.)
 constexpr int kSortCtas = 8;            // one cluster sorts: bins and counts meet in shared memory
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -241,7 +242,11 @@ struct GradArgs {
     int chunk;                   // sorted tokens per chunk of the reduction
     int64_t nchunks;
     uint32_t *named;             // bit v: a token names row v (when the gradient is written, not added)
-    int zero_rows;               // rows a CTA zeroes
+    // CTAs (along x) that sort and that sum.  Those behind them zero rows of the table, sort_rows or sum_rows each: the
+    // first `early` beside the sort, the others beside the sums.
+    int sort_ctas, sum_ctas;
+    int sort_rows, sum_rows;
+    int64_t early;
     float *part;                 // [nchunks][2][H] partial sums: of the run at a chunk's first token, of its last run
 };
 
@@ -309,8 +314,9 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t n, uint32_t *wsum, int
     return base + incl - n;
 }
 
-// Radix sort, least significant digit first, by one CTA (up to 2048 tokens) or by the cluster of kSortCtas (up to
-// 131072), with a CTA's tokens in registers.  Whole gradient of rows of 64, one CTA / cluster: 11.4 / 14.4 us at 1024
+// Radix sort, least significant digit first, by one CTA (up to 2048 tokens; 4096 where a large table is written) or by the
+// cluster of kSortCtas (up to 131072), with a CTA's tokens in registers (16 a thread, from 32769 tokens on, spill 176 bytes
+// under the 64 registers that 1024 threads leave).  Whole gradient of rows of 64, one CTA / cluster: 11.4 / 14.4 us at 1024
 // tokens, 15.0 / 15.9 at 2048, 20.2 / 17.5 at 4096; held in registers / swept from memory (below): 34.9 / 40.4 us
 // at 32768, 89.7 / 96.5 at 131072.  Tokens are dealt in order to CTAs, warps and rounds of 32, so a
 // token's place among equal digits is the count in lower CTAs, in lower warps, in its warp's earlier rounds and
@@ -318,6 +324,7 @@ __device__ __forceinline__ uint32_t scan_threads(uint32_t n, uint32_t *wsum, int
 // writes to global memory comes in runs (scattered 4-byte stores kept one SM busy for 25 us per 16384 tokens).
 constexpr int kCtaRounds = 16;                       // most rounds of 1024 tokens a CTA holds
 constexpr int kOneTokens = 2 * kSortThreads;
+constexpr int kOneWritten = 4 * kSortThreads;         // of a large table that is written, see zero_rows
 constexpr int kHeldTokens = kCtaRounds * kSortThreads * kSortCtas;
 constexpr int kHeldWords = kSortWarps * kMaxBins + 4 * kMaxBins + 64;
 constexpr int held_smem(int rounds) { return 4 * kHeldWords + 8 * kSortThreads * rounds; }
@@ -484,65 +491,107 @@ __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads
         if (id >= 0 && id < a.V && id != a.pad) atomicOr(a.named + (id >> 5), 1u << (id & 31));
     }
 }
+// Zero: CTAs come in the order of the table.  (A grid of two CTAs per SM that strides over the rows wrote 6.0 TB/s, this
+// order 7.2: what is written at any time lies close together.)  What is zeroed where, us a call from bf16 rows of 1024 into
+// fp32 tables:
+// - up to 2048 tokens the whole table beside the sort of one CTA, where marking and zeroing beside the sums took 25.8 for
+//   20.2 (2047 into 16000 rows) and 14.2 for 11.9 (300 into 1000).  With 16 / 32 / 64 KB a CTA there: 20.1 / 18.7 / 20.8 at
+//   2047 into 4000 rows, 36.3 / 32.0 / 29.7 into 32000.
+// - so too up to 4096 tokens from 40 MB of table on: the slower sort is hidden then (4096 tokens, by one CTA / by the
+//   cluster: 26.1 / 24.6 into 16 MB, 28.6 / 30.7 into 65 MB, 35.6 / 36.9 into 131 MB).
+// - else beside the sums, but from 56 MB of table on for a share beside the cluster that sorts (6000 tokens, with the
+//   share / without: 31.6 / 29.5 into 49 MB, 38.1 / 45.3 into 131 MB).  Clusters of zeroing CTAs 2 / 6 / 9 / 14, with as much
+//   in all: 140 / 123 / 118 / 114 at 8192 x 4096 into 32000 rows.
+constexpr int kRedThreads = 128;                          // of the kernels that sum
+constexpr int kZeroBytes = 16384;                         // of a CTA beside the sums
+constexpr int kZeroWords = kZeroBytes / 16 / 32 + 1;      // words of bits of its rows, at 16 bytes a row
+constexpr int kOneZeroBytes = 32768;                      // of a CTA beside the sort of one CTA
+constexpr int64_t kOneTable = 40 << 20;                   // bytes of a table from which up to kOneWritten tokens are sorted by one
+constexpr int kEarlyBytes = 524288;                       // of a CTA beside the cluster that sorts
+constexpr int64_t kEarlyTable = 56 << 20;                 // bytes of a table from which there are such CTAs
+constexpr int kEarlyClusters = 14;                        // clusters of them: 15 of 8 SMs fit at once
+enum { kZeroAll = 0, kZeroMarked = 1, kZeroFew = 2 };     // every row; those without a mark; those not among the few ids
+// Zeroes rows [r0, end) of dE.  bits: room for a bit a row.
+template <int kThreads, int kWhich>
+__device__ __forceinline__ void zero_rows(const GradArgs &a, int64_t r0, int64_t end, uint32_t *bits) {
+    if (r0 >= end) return;      // the last CTAs may go past what there is
+    const int64_t row_words = a.H * (a.de_bf16 ? 2 : 4) / 16, b0 = r0 >> 5;
+    uint4 *dst = static_cast<uint4 *>(a.dE) + r0 * row_words;
+    if (kWhich == kZeroAll) {
+        const int64_t all = (end - r0) * row_words;
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < all; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int words = static_cast<int>(((end - 1) >> 5) - b0) + 1;
+    for (int i = threadIdx.x; i < words; i += kThreads) bits[i] = kWhich == kZeroFew ? 0u : __ldcg(a.named + b0 + i);
+    __syncthreads();
+    if (kWhich == kZeroFew) {   // the CTA looks for its own rows among the ids
+        for (int t = threadIdx.x; t < a.T; t += kThreads) {
+            const int64_t id = id_at(a.ids, t);
+            if (id >= r0 && id < end && id != a.pad) atomicOr(bits + ((id >> 5) - b0), 1u << (id & 31));
+        }
+        __syncthreads();
+    }
+    auto named = [&](int64_t r) { return (bits[(r >> 5) - b0] >> (r & 31)) & 1u; };
+    if (row_words >= kThreads) {
+        for (int64_t r = r0; r < end; ++r, dst += row_words) {
+            if (named(r)) continue;
+#pragma unroll 4
+            for (int64_t i = threadIdx.x; i < row_words; i += kThreads) dst[i] = make_uint4(0, 0, 0, 0);
+        }
+    } else {
+        // short rows: the CTA's words (at most kEarlyBytes / 16) as one run
+        const uint32_t all = static_cast<uint32_t>((end - r0) * row_words), rw = static_cast<uint32_t>(row_words);
+#pragma unroll 4
+        for (uint32_t i = threadIdx.x; i < all; i += kThreads)
+            if (!named(r0 + i / rw)) dst[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+// what a CTA behind those that sort, or behind those that sum, zeroes
+template <int kWhich>
+__device__ __forceinline__ void zero_beside_sort(const GradArgs &a, uint32_t *smem) {
+    const int64_t r0 = int64_t(blockIdx.x - a.sort_ctas) * a.sort_rows;
+    zero_rows<kSortThreads, kWhich>(a, r0, min(r0 + a.sort_rows, a.early), smem);
+}
+template <int kWhich>
+__device__ __forceinline__ void zero_beside_sums(const GradArgs &a) {
+    __shared__ uint32_t s_named[kZeroWords];
+    const int64_t r0 = a.early + (int64_t(blockIdx.y) * (gridDim.x - a.sum_ctas) + (blockIdx.x - a.sum_ctas)) * a.sum_rows;
+    zero_rows<kRedThreads, kWhich>(a, r0, min(r0 + a.sum_rows, a.V), s_named);
+}
+
 template <int kRounds>
-__global__ void __launch_bounds__(kSortThreads) embed_sort_one_kernel(const GradArgs a, int rounds) {
+__global__ void __launch_bounds__(kSortThreads, 2) embed_sort_one_kernel(const GradArgs a, int rounds) {
     extern __shared__ uint32_t sort_smem[];
-    pdl_wait();                 // before the release: what starts after this kernel may rely on ids and marks
+    pdl_wait();
     pdl_launch_dependents();
+    if (blockIdx.x >= a.sort_ctas) {
+        zero_beside_sort<kZeroAll>(a, sort_smem);
+        return;
+    }
     sort_held<false, kRounds>(a, sort_smem, rounds);
 }
 template <int kRounds>
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort_held_kernel(const GradArgs a, int rounds) {
     extern __shared__ uint32_t sort_smem[];
-    pdl_wait();                 // before the release: what starts after this kernel may rely on ids and marks
+    pdl_wait();
     pdl_launch_dependents();
+    if (blockIdx.x >= a.sort_ctas) {
+        zero_beside_sort<kZeroMarked>(a, sort_smem);
+        return;
+    }
     sort_held<true, kRounds>(a, sort_smem, rounds);
 }
 __global__ void __cluster_dims__(kSortCtas, 1, 1) __launch_bounds__(kSortThreads, 1) embed_sort_swept_kernel(const GradArgs a) {
     extern __shared__ uint32_t sort_smem[];
-    pdl_wait();                 // before the release: what starts after this kernel may rely on ids and marks
+    pdl_wait();
     pdl_launch_dependents();
+    if (blockIdx.x >= a.sort_ctas) {
+        zero_beside_sort<kZeroMarked>(a, sort_smem);
+        return;
+    }
     sort_swept(a, sort_smem);
-}
-
-// Zero: a CTA of 256 threads for up to 16 KB of rows, in the order of the table.  (A grid of two CTAs per SM
-// that strides over the rows wrote 6.0 TB/s, this order 7.2: what is written at any time lies close together.)
-constexpr int kZeroThreads = 256;
-constexpr int kZeroBytes = 16384;
-constexpr int kZeroWords = kZeroBytes / 16 / 32 + 1;      // words of bits of a CTA's rows, at 16 bytes a row
-template <bool kFew>
-__global__ void __launch_bounds__(kZeroThreads) embed_zero_kernel(const GradArgs a) {
-    __shared__ uint32_t s_named[kZeroWords];
-    pdl_launch_dependents();
-    if (a.T == 0) pdl_wait();   // otherwise the kernels before have let this one start, after a wait for ids and marks
-    const int64_t row_words = a.H * (a.de_bf16 ? 2 : 4) / 16;
-    const int64_t r0 = blockIdx.x * int64_t(a.zero_rows), end = min(r0 + a.zero_rows, a.V), b0 = r0 >> 5;
-    const int words = static_cast<int>(((end - 1) >> 5) - b0) + 1;
-    for (int i = threadIdx.x; i < words; i += kZeroThreads) s_named[i] = kFew || a.T == 0 ? 0u : __ldcg(a.named + b0 + i);
-    __syncthreads();
-    if (kFew) {                 // no marks: the CTA looks for its own rows among the few ids
-        for (int t = threadIdx.x; t < a.T; t += kZeroThreads) {
-            const int64_t id = id_at(a.ids, t);
-            if (id >= r0 && id < end && id != a.pad) atomicOr(s_named + ((id >> 5) - b0), 1u << (id & 31));
-        }
-        __syncthreads();
-    }
-    auto named = [&](int64_t r) { return (s_named[(r >> 5) - b0] >> (r & 31)) & 1u; };
-    uint4 *dst = static_cast<uint4 *>(a.dE) + r0 * row_words;
-    if (row_words >= kZeroThreads) {
-        for (int64_t r = r0; r < end; ++r, dst += row_words) {
-            if (named(r)) continue;
-#pragma unroll 4
-            for (int64_t i = threadIdx.x; i < row_words; i += kZeroThreads) dst[i] = make_uint4(0, 0, 0, 0);
-        }
-    } else {
-        // short rows: the CTA's words (at most 1024) as one run
-        const uint32_t all = static_cast<uint32_t>((end - r0) * row_words), rw = static_cast<uint32_t>(row_words);
-#pragma unroll 4
-        for (uint32_t i = threadIdx.x; i < all; i += kZeroThreads)
-            if (!named(r0 + i / rw)) dst[i] = make_uint4(0, 0, 0, 0);
-    }
-    if (blockIdx.x == gridDim.x - 1) pdl_wait();
 }
 
 // kN (4 or 8) elements of a row of dY or dE as loaded, and as floats
@@ -596,7 +645,6 @@ __device__ __forceinline__ void write_row(const GradArgs &a, uint32_t row, int64
 
 // Reduce: block (chunk, column tile); a thread owns 8 columns and walks the chunk's tokens in order,
 // kBatch rows of dY in flight, with the old rows of dE that they will be added to.
-constexpr int kRedThreads = 128;
 constexpr int kRedCols = kRedThreads * 8;
 constexpr int kMaxChunk = 128;
 constexpr int kBatch = 4;
@@ -605,6 +653,10 @@ __global__ void __launch_bounds__(kRedThreads) embed_reduce_kernel(const GradArg
     __shared__ uint32_t s_id[kMaxChunk + 2], s_pos[kMaxChunk];   // s_id[0]: the token before the chunk; last + 1: after it
     pdl_launch_dependents();
     pdl_wait();
+    if (!kAdd && blockIdx.x >= a.sum_ctas) {
+        zero_beside_sums<kZeroMarked>(a);
+        return;
+    }
     const uint32_t *ids = a.key[a.passes & 1], *pos = a.pos[a.passes & 1];
     const int64_t ch = blockIdx.x;
     const int64_t i0 = ch * a.chunk;
@@ -665,8 +717,12 @@ constexpr int kFewRun = 4;
 template <bool kDyBf16, bool kDeBf16, bool kAdd>
 __global__ void __launch_bounds__(kRedThreads) embed_few_kernel(const GradArgs a) {
     __shared__ uint32_t s_key[kFewTokens], s_id[kFewTokens + 2], s_pos[kFewTokens];   // s_id as in embed_reduce_kernel
-    pdl_wait();                 // before the release: `zero` may rely on the ids
+    pdl_wait();
     pdl_launch_dependents();
+    if (!kAdd && blockIdx.x >= a.sum_ctas) {
+        zero_beside_sums<kZeroFew>(a);
+        return;
+    }
     const int tid = threadIdx.x, T = static_cast<int>(a.T);
     const uint32_t V = static_cast<uint32_t>(a.V);
     for (int t = tid; t < T; t += kRedThreads) s_key[t] = key_of(a, t);

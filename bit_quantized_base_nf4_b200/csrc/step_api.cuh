@@ -174,31 +174,49 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
     QL_TRY(require_sm100());
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int variant = 4 * dy_is_bf16 + 2 * de_is_bf16 + accumulate;
-    const bool few = T > 0 && T <= emb::kFewTokens;
+    const bool few = T <= emb::kFewTokens;
+    // what is zeroed beside the sort and beside the sums (the rules stand at zero_rows)
+    const int64_t row_bytes = H * (de_is_bf16 ? 2 : 4), table = accumulate ? 0 : V * row_bytes;
+    const bool one = T <= (table >= emb::kOneTable ? emb::kOneWritten : emb::kOneTokens);
+    a.sort_ctas = one ? 1 : emb::kSortCtas;
+    a.sum_ctas = static_cast<int>(few ? ceil_div(T, emb::kFewRun) : a.nchunks);
+    int64_t early_ctas = 0, zero_columns = 0;
+    if (!accumulate) {
+        const auto rows_of = [&](int64_t bytes) { return std::min(V, std::max<int64_t>(1, bytes / row_bytes)); };
+        if (!few && (one || table >= emb::kEarlyTable)) {
+            const int64_t beside = emb::kEarlyClusters * emb::kSortCtas;
+            const int64_t rows = one ? rows_of(emb::kOneZeroBytes) : std::min(rows_of(emb::kEarlyBytes), ceil_div(V, 2 * beside));
+            a.early = one ? V : std::min(V, rows * beside);
+            a.sort_rows = static_cast<int>(rows);
+            early_ctas = ceil_div(ceil_div(a.early, rows), a.sort_ctas) * a.sort_ctas;      // whole clusters
+        }
+        a.sum_rows = static_cast<int>(rows_of(emb::kZeroBytes));
+        zero_columns = ceil_div(ceil_div(V - a.early, a.sum_rows), tiles);
+    }
+    const dim3 sort_grid(static_cast<unsigned>(a.sort_ctas + early_ctas));
+    const dim3 sum_grid(static_cast<unsigned>(a.sum_ctas + zero_columns), static_cast<unsigned>(tiles));
     if (few) {
         void (*const sum[8])(emb::GradArgs) = {
             emb::embed_few_kernel<false, false, false>, emb::embed_few_kernel<false, false, true>,
             emb::embed_few_kernel<false, true, false>,  emb::embed_few_kernel<false, true, true>,
             emb::embed_few_kernel<true, false, false>,  emb::embed_few_kernel<true, false, true>,
             emb::embed_few_kernel<true, true, false>,   emb::embed_few_kernel<true, true, true>};
-        QL_TRY(launch_pdl("embed_few_kernel launch", sum[variant],
-                          dim3(static_cast<unsigned>(ceil_div(T, emb::kFewRun)), static_cast<unsigned>(tiles)), emb::kRedThreads, 0, st, a));
-    } else if (T > 0) {
-        if (!accumulate)
+        QL_TRY(launch_pdl("embed_few_kernel launch", sum[variant], sum_grid, emb::kRedThreads, 0, st, a));
+    } else {
+        if (!accumulate && !one)
             QL_TRY(launch_pdl("embed_mark_kernel launch", emb::embed_mark_kernel, dim3(emb::kSortCtas), emb::kSortThreads, 0, st, a));
         if (T <= emb::kHeldTokens) {
-            const bool one = T <= emb::kOneTokens;
             const int rounds = static_cast<int>(ceil_div(T, int64_t(one ? 1 : emb::kSortCtas) * emb::kSortThreads));
             void (*sort)(emb::GradArgs, int);
-            if (one) sort = rounds == 1 ? emb::embed_sort_one_kernel<1> : emb::embed_sort_one_kernel<2>;
+            if (one) sort = rounds == 1 ? emb::embed_sort_one_kernel<1> : rounds == 2 ? emb::embed_sort_one_kernel<2> : emb::embed_sort_one_kernel<4>;
             else if (rounds <= 2) sort = emb::embed_sort_held_kernel<2>;
             else sort = rounds <= 4 ? emb::embed_sort_held_kernel<4> : emb::embed_sort_held_kernel<emb::kCtaRounds>;
             QL_TRY(set_smem(sort, emb::held_smem(rounds)));
-            QL_TRY(launch_pdl("embed_sort kernel launch", sort, dim3(one ? 1 : emb::kSortCtas), emb::kSortThreads,
+            QL_TRY(launch_pdl("embed_sort kernel launch", sort, sort_grid, emb::kSortThreads,
                               emb::held_smem(rounds), st, a, rounds));
         } else {
             QL_TRY(set_smem(emb::embed_sort_swept_kernel, emb::kSortSmem));
-            QL_TRY(launch_pdl("embed_sort_swept_kernel launch", emb::embed_sort_swept_kernel, dim3(emb::kSortCtas),
+            QL_TRY(launch_pdl("embed_sort_swept_kernel launch", emb::embed_sort_swept_kernel, sort_grid,
                               emb::kSortThreads, emb::kSortSmem, st, a));
         }
         void (*const reduce[8])(emb::GradArgs) = {
@@ -206,17 +224,11 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
             emb::embed_reduce_kernel<false, true, false>,  emb::embed_reduce_kernel<false, true, true>,
             emb::embed_reduce_kernel<true, false, false>,  emb::embed_reduce_kernel<true, false, true>,
             emb::embed_reduce_kernel<true, true, false>,   emb::embed_reduce_kernel<true, true, true>};
-        QL_TRY(launch_pdl("embed_reduce_kernel launch", reduce[variant],
-                          dim3(static_cast<unsigned>(a.nchunks), static_cast<unsigned>(tiles)), emb::kRedThreads, 0, st, a));
+        QL_TRY(launch_pdl("embed_reduce_kernel launch", reduce[variant], sum_grid, emb::kRedThreads, 0, st, a));
         // (more than kFewTokens tokens are more than one chunk)
         QL_TRY(launch_pdl("embed_join_kernel launch", de_is_bf16 ? emb::embed_join_kernel<true> : emb::embed_join_kernel<false>,
                           dim3(static_cast<unsigned>(ceil_div(a.nchunks - 1, emb::kJoinWarps)), static_cast<unsigned>(jtiles)),
                           emb::kJoinWarps * 32, 0, st, a));
-    }
-    if (!accumulate) {
-        a.zero_rows = static_cast<int>(std::min<int64_t>(V, std::max<int64_t>(1, emb::kZeroBytes / (H * (de_is_bf16 ? 2 : 4)))));
-        QL_TRY(launch_pdl("embed_zero_kernel launch", few ? emb::embed_zero_kernel<true> : emb::embed_zero_kernel<false>,
-                          dim3(static_cast<unsigned>(ceil_div(V, a.zero_rows))), emb::kZeroThreads, 0, st, a));
     }
     return QLORA_OK;
 }

@@ -176,3 +176,13 @@ def test_grad_right_behind_the_writers_of_its_inputs_and_before_a_reader(T):
     for (i, d), x in zip(new, got):
         want = torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, i, d.double()).float()
         assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("T", [193, 2047, 2049, 3001, 4096, 4097, 9001, 40_000, 140_000])
+@pytest.mark.parametrize("V,H,det", [(20_000, 520, F32), (20_001, 536, F32), (30_011, 520, F32), (9_001, 4104, BF16), (700_001, 24, F32), (3, 5_000_008, F32)])
+def test_grad_written_into_large_tables(T, V, H, det):
+    # tables around and above the sizes from which another sort is taken and rows are zeroed beside it
+    if T * H > 400_000_000:
+        T = 200 + T % 7                                    # (rows of 20 MB: a few tokens are enough)
+    for how in ("zipf", "one"):
+        _check_grad(T, V, H, how, False, BF16, det, pad=2 if how == "zipf" and V > 3 else -1)
