@@ -186,3 +186,71 @@ def test_grad_written_into_large_tables(T, V, H, det):
         T = 200 + T % 7                                    # (rows of 20 MB: a few tokens are enough)
     for how in ("zipf", "one"):
         _check_grad(T, V, H, how, False, BF16, det, pad=2 if how == "zipf" and V > 3 else -1)
+
+
+# ----------------------------------------------------------------- ends of the ranges
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [1.0, 0.01, -3e-39, 1e30, 0.0])
+def test_lookup_of_subnormal_huge_and_infinite_values(dtype, scale):
+    x = torch.tensor([0.0, -0.0, 1e-38, -3e-39, 1.4e-45, 2 ** -126, 1.17e-38, 3e38, -3e38, 1e9, 7e-9, 65504.0, float("inf"), 1.0, -1.0, 3.3e38])
+    table = x.to(dtype).repeat(3, 1).to(DEV)
+    for out in (F32, BF16):
+        Y = torch.empty(4, 16, dtype=out, device=DEV)
+        q.qlora_embed_fwd(table, torch.tensor([2, 0, 1, 1], device=DEV), scale, Y)
+        want = (table[0].double() * float(np.float32(scale))).float().to(out)
+        for row in Y:
+            nan = torch.isnan(want)
+            assert torch.equal(torch.isnan(row), nan)
+            word = torch.int32 if out == F32 else torch.int16
+            assert torch.equal(row.view(word)[~nan], want.view(word)[~nan])
+
+
+@pytest.mark.parametrize("T", [1, 5, 192, 300, 3000, 9000, 140_000])
+@pytest.mark.parametrize("acc", [False, True])
+def test_grad_of_bad_ids_alone(T, acc):
+    V, H = 50, 24
+    ids = torch.full((T,), V, device=DEV)
+    ids[::2] = -1
+    dY, dE = torch.full((T, H), float("nan"), device=DEV), torch.full((V, H), 3.0, device=DEV)
+    ws = torch.empty(q.qlora_embed_grad_workspace_bytes(T, V, H), dtype=torch.uint8, device=DEV).fill_(0xFF)
+    q.qlora_embed_grad(ids, dY, 1.0, dE, accumulate=acc, ws=ws)
+    with pytest.raises(q.QloraError, match="token id"):
+        q.qlora_sync_status()
+    assert (dE == (3.0 if acc else 0.0)).all()
+
+
+@pytest.mark.parametrize("T", [100, 2000, 9000])
+@pytest.mark.parametrize("acc", [False, True])
+def test_grad_of_a_table_beyond_32_bits_of_elements(T, acc):
+    V, H = 530_000, 8192                                   # 2^32 + elements
+    g = torch.Generator(device=DEV).manual_seed(T)
+    rows = torch.tensor([0, 262_143, 262_144, 262_145, 524_287, 524_288, V - 1], device=DEV)
+    ids = rows[torch.randint(0, 7, (T,), generator=g, device=DEV)]
+    dY = torch.randint(-3, 4, (T, H), generator=g, device=DEV).to(BF16)
+    dE = torch.empty(V, H, dtype=BF16, device=DEV).fill_(1.0 if acc else float("nan"))
+    ws = torch.empty(q.qlora_embed_grad_workspace_bytes(T, V, H), dtype=torch.uint8, device=DEV)
+    q.qlora_embed_grad(ids, dY, 0.5, dE, accumulate=acc, ws=ws)
+    q.qlora_sync_status()
+    for r in rows.tolist():
+        want = 0.5 * dY[ids == r].double().sum(dim=0) + (1.0 if acc else 0.0)
+        assert torch.equal(dE[r], want.float().to(BF16)), r
+        dE[r] = 1.0 if acc else 0.0
+    for lo in range(0, V, 50_000):
+        assert (dE[lo:lo + 50_000] == (1.0 if acc else 0.0)).all()
+
+
+def test_grad_of_tokens_beyond_32_bits_of_elements():
+    T, V, H = 270_001, 900, 16_384                         # 2^32 + elements of dY
+    g = torch.Generator(device=DEV).manual_seed(1)
+    ids = torch.randint(0, V, (T,), generator=g, device=DEV)
+    dY = torch.empty(T, H, dtype=BF16, device=DEV)
+    for lo in range(0, T, 30_000):
+        dY[lo:lo + 30_000] = torch.randint(-3, 4, dY[lo:lo + 30_000].shape, generator=g, device=DEV, dtype=torch.int8)
+    dE = torch.empty(V, H, device=DEV)
+    ws = torch.empty(q.qlora_embed_grad_workspace_bytes(T, V, H), dtype=torch.uint8, device=DEV)
+    q.qlora_embed_grad(ids, dY, 1.0, dE, ws=ws)
+    q.qlora_sync_status()
+    for c in (0, 8000, H - 64):
+        want = torch.zeros(V, 64, dtype=torch.float64, device=DEV).index_add_(0, ids, dY[:, c:c + 64].double())
+        assert torch.equal(dE[:, c:c + 64], want.float())

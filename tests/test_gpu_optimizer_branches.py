@@ -215,3 +215,66 @@ def test_norm_misses_no_chunk():
         x[at] = 0.0
     q.qlora_sync_status()
     assert out[:len(places), 0].tolist() == [3.0] * len(places)
+
+
+def test_norm_of_nothing():
+    for sizes in ([0], [0, 0, 0]):
+        plan = q.qlora_adamw_plan_init([q.AdamWTensor(None, torch.empty(n, device=DEV)) for n in sizes])
+        out = torch.full((2,), float("nan"), device=DEV)
+        q.qlora_grad_norm(plan, 1e-7, out)
+        q.qlora_sync_status()
+        assert out[0] == 0 and abs(out[1].item() - 0.1) <= 2.0 ** -23
+
+
+# ----------------------------------------------------------------- beyond 32 bits of elements
+
+WINDOWS = [0, (1 << 31) - 512, (1 << 32) - 1024, (1 << 32)]       # each starts at a block of 256 and holds 1024 elements
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_tensor_beyond_32_bits_of_elements(bits):
+    n = (1 << 32) + 4097
+    g = torch.Generator(device=DEV).manual_seed(7)
+    grad, param = torch.zeros(n, dtype=BF16, device=DEV), torch.zeros(n, dtype=BF16, device=DEV)
+    for w in WINDOWS + [n // 256 * 256 - 1024]:                     # the last one, and what lies behind the last whole block
+        grad[w:w + 1024] = _rand(g, 1024).to(BF16)
+    grad[n - 1] = 0.5
+    t = q.AdamWTensor.zeros(param, grad, bits=bits)
+    plan, out = q.qlora_adamw_plan_init([t]), torch.empty(2, device=DEV)
+    q.qlora_grad_norm(plan, float("inf"), out)
+    q.qlora_adamw_step(plan, 1e-3, 1)
+    q.qlora_sync_status()
+    total = math.fsum(float(grad[lo:lo + (1 << 26)].double().square().sum()) for lo in range(0, n, 1 << 26))
+    assert abs(out[0].item() - math.sqrt(total)) <= 2.0 ** -23 * math.sqrt(total)
+    for w in WINDOWS + [n // 256 * 256 - 1024]:
+        s = slice(w, min(w + 1024 + (n % 256 if w + 1024 == n // 256 * 256 else 0), n))
+        b = slice(s.start // 256, -(-s.stop // 256))
+        part = q.AdamWTensor(param[s], grad[s], t.exp_avg[s], t.exp_avg_sq[s], t.exp_avg_step[b] if bits == 8 else None,
+                             t.exp_avg_sq_step[b] if bits == 8 else None)
+        ref = Ref(part)
+        ref.p.zero_()
+        ref.step(1, 1e-3, None, 1e-8, f"window at {w}")
+    live = sum(int((x != 0).sum()) for x in param.split(1 << 28))
+    assert live == sum(int((x != 0).sum()) for x in grad.split(1 << 28))
+
+
+def test_adam8_beyond_32_bits_of_elements():
+    n = (1 << 32) + 300
+    g = torch.Generator(device=DEV).manual_seed(8)
+    x = torch.zeros(n, device=DEV)
+    at = WINDOWS[:3] + [n // 256 * 256 - 768]
+    for w in at:
+        x[w:w + 1024] = _rand(g, min(1024, n - w))
+    codes, steps = torch.empty(n, dtype=torch.int8, device=DEV), torch.empty(-(-n // 256), device=DEV)
+    q.qlora_adam8_encode(x, codes, steps)
+    kept = []
+    for w in at:
+        e = min(w + 1024, n)
+        k, d = _encode(x[w:e].double(), 127)
+        assert torch.equal(codes[w:e].double(), k) and torch.equal(steps[w // 256:-(-e // 256)].double(), d)
+        kept.append((w, e, _decode(k, d)))
+    q.qlora_adam8_decode(codes, steps, x)
+    q.qlora_sync_status()
+    for w, e, v in kept:
+        assert torch.equal(x[w:e].double(), v)
+    assert sum(int((c != 0).sum()) for c in codes.split(1 << 28)) == sum(int((c != 0).sum()) for c in x.split(1 << 28))
