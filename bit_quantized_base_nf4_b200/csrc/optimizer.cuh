@@ -1,10 +1,13 @@
 // optimizer.cuh -- AdamW over many tensors in one launch (states in 32 bits or in 8 bits),
 // the global gradient norm with its clip coefficient, and the 8-bit state code.
 //
-// One step, per element, every operation rounded to float32:
+// One step, per element:
 //   g = grad (* clip coefficient)
 //   m = b1 m + (1 - b1) g,   v = b2 v + (1 - b2) g^2
 //   p = p - lr (decay p + (m / (1 - b1^t)) / (sqrt(v) / sqrt(1 - b2^t) + eps))
+// g, m and v are rounded to float32 operation by operation.  p takes an approximate root and reciprocal (2^-23 each),
+// denominators sqrt(v) ds + de with the corrections worked out beforehand, and fused multiply-adds: at most 11 half steps
+// of float32 relative to lr (|decay p| + |u|) before its own rounding, 16 in the interface.
 //
 // 8-bit states: blocks of 256 values with one fp32 step d each, value = k |k| d, where x is
 // m (k in -127 .. 127) or sqrt(v) (k in 0 .. 255; the second moment is the value's square).
@@ -14,7 +17,7 @@
 // block's largest) at a bounded cost for its large ones (half a step is 0.8 % and 0.4 % at
 // the top).  sqrt(v) is stored, not v, so that m and the denominator keep the same range.
 // All roundings up to the code are fixed (no fused multiply-add), so codes are bit-exact.
-// A block with a non-finite value stores d = NaN and k = 0: every later step on it is NaN.
+// A block with a non-finite value (or a negative v) stores d = NaN and k = 0: every later step on it is NaN.
 // d below 2^-126, where 1 / d could overflow, is stored as 0 with k = 0.
 #pragma once
 

@@ -322,20 +322,24 @@ qlora_status qlora_embed_grad(const void *ids, int ids_bytes, int64_t T, const v
  * dB of qlora_lora_grad_AB, and of any other trained tensor (the "5.8 QLoRA"
  * page's optimizer paragraph and the "Quantized vs. non-quantized weights" page,
  * section 4.3: AdamW with its states in 8 bits; the pages print no code table).
- * Step t, per element, every operation rounded to float32:
+ * Step t, per element:
  *   g = grad * (*grad_scale)                     (grad alone without grad_scale)
  *   m = beta1 m + (1 - beta1) g
  *   v = beta2 v + (1 - beta2) g^2
  *   p = p - lr lr_scale (weight_decay p + (m / (1 - beta1^t)) /
  *                                         (sqrt(v) / sqrt(1 - beta2^t) + eps))
+ * g, m and v take one rounding to float32 an operation.  p is worked out with an
+ * approximate root and reciprocal, the bias corrections folded into the denominator
+ * and fused multiply-adds: before its last rounding it is within 16 * 2^-24 of
+ * lr lr_scale (|weight_decay p| + |u|), u the quotient, of the formula.
  * 8-bit states hold blocks of 256 consecutive values (the last block of a tensor
  * may be shorter) as k |k| d: one fp32 step d per block and an int8 k in
  * -127..127 for m, a uint8 k in 0..255 for sqrt(v).  With K = 127 or 255 and
  * RN = rounding to float32:
  *   d = RN(max |x| / K^2),  y = RN(|x| RN(1 / d)),
  *   |k| = the number of integers j >= 0 with y > j^2 + j + 1/2.
- * d below 2^-126 is stored as 0 with k = 0; a block that holds an infinity or a
- * NaN stores d = NaN and k = 0.  Reading back: m = RN(RN(k |k|) d),
+ * d below 2^-126 is stored as 0 with k = 0; a block that holds an infinity, a NaN
+ * or a negative v stores d = NaN and k = 0.  Reading back: m = RN(RN(k |k|) d),
  * v = RN(w^2) with w = RN(k^2 d).  m, v and the codes are bit-exact (no fused
  * multiply-add up to the code). */
 enum {
@@ -394,6 +398,7 @@ qlora_status qlora_adamw_plan_init(const qlora_adamw_tensor *tensors, int64_t co
  *   grad_scale: device float32, the clip coefficient (out + 1 of qlora_grad_norm),
  *     or NULL.  A value that is not finite makes the step change nothing (the
  *     counter included).
+ * A plan with QLORA_OPT_GRAD_ONLY tensors is refused: it serves the norm alone.
  * 0 <= beta < 1, lr >= 0, and eps = 0 or eps (1 - beta1) >= 2^-126 (with eps = 0 an
  * element whose v is zero becomes NaN or infinite, as in the formula).  The plan buffer holds scratch: two calls on
  * one plan whose work overlaps in time race. */
