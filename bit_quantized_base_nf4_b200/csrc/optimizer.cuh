@@ -441,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 4) adamw32_kernel(const StepArgs a) 
     }
 }
 
-// ---- 8-bit states: 10 to 18 bytes per parameter.  The codes cost some 50 instructions per parameter, so
-// instruction issue takes longer than HBM, and a block's dependent chain (absmax, division, root, code) is as
+// ---- 8-bit states: 10 to 18 bytes per parameter.  A step takes 62 instructions per parameter, which take longer than HBM
+// (69 % of the issue slots used at 24 warps an SM), and a block's dependent chain (absmax, division, root, code) is as
 // long as a load.  So each warp streams its elements through two stages of 512 in shared memory by
 // asynchronous copies, one stage ahead of the two blocks it works on.  A lane copies exactly what it reads
 // back itself, so the ring needs no barrier; copies past a tensor's end are zero-filled.
