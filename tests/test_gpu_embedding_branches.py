@@ -254,3 +254,33 @@ def test_grad_of_tokens_beyond_32_bits_of_elements():
     for c in (0, 8000, H - 64):
         want = torch.zeros(V, 64, dtype=torch.float64, device=DEV).index_add_(0, ids, dY[:, c:c + 64].double())
         assert torch.equal(dE[:, c:c + 64], want.float())
+
+
+@pytest.mark.parametrize("T,V,H", [(100, 9000, 264), (1500, 9000, 264), (3001, 20_500, 520), (9001, 30_100, 520), (140_000, 30_100, 520)])
+def test_written_grad_captured_and_replayed_on_two_streams_at_once(T, V, H):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    work = []
+    for _ in range(2):
+        ids, dY = torch.zeros(T, dtype=torch.int64, device=DEV), torch.zeros(T, H, dtype=BF16, device=DEV)
+        dE, ws = torch.empty(V, H, device=DEV), torch.empty(q.qlora_embed_grad_workspace_bytes(T, V, H), dtype=torch.uint8, device=DEV)
+        graph, stream, copies = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.empty(2, V, H, device=DEV)
+        with torch.cuda.graph(graph):
+            for i in range(2):                             # twice, with the same scratch; dE is read in between
+                dE.fill_(float("nan"))
+                q.qlora_embed_grad(ids, dY, 1.0, dE, padding_id=1, ws=ws)
+                copies[i].copy_(dE)
+        work.append((ids, dY, graph, stream, copies, dE, ws))      # (kept: the graph writes to their addresses)
+    for how in ("zipf", "any", "one", "runs", "zipf"):
+        for ids, dY, *_ in work:
+            ids.copy_(_ids(g, T, V, how)), dY.copy_(torch.randint(-3, 4, (T, H), generator=g, device=DEV))
+        torch.cuda.synchronize()
+        for _, _, graph, stream, *_ in work:
+            with torch.cuda.stream(stream):
+                graph.replay()
+                graph.replay()
+        torch.cuda.synchronize()
+        q.qlora_sync_status()
+        for ids, dY, _, _, copies, *_ in work:
+            live = ids != 1
+            want = torch.zeros(V, H, dtype=torch.float64, device=DEV).index_add_(0, ids[live], dY[live].double()).float()
+            assert torch.equal(copies[0], want) and torch.equal(copies[1], want), how
